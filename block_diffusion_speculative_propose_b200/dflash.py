@@ -30,7 +30,7 @@ STATUS = {
     -9: "DFLASH_ERR_EXCHANGE",
 }
 DEVERR_TIMEOUT, DEVERR_SLOT, DEVERR_TABLE, DEVERR_TOKEN, DEVERR_POSITION = 1, 2, 4, 8, 16
-KERNEL_KINDS = 14
+KERNEL_KINDS = 17
 
 
 class DFlashError(RuntimeError):
@@ -116,6 +116,7 @@ def lib() -> ctypes.CDLL:
                            "block_diffusion_speculative_propose_b200/build.py")
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    i64 = ctypes.c_int64
     sig = {
         "dflash_create": ([ctypes.POINTER(_Config), ctypes.POINTER(_Weights), i32,
                            ctypes.POINTER(vp)], i32),
@@ -162,6 +163,8 @@ def lib() -> ctypes.CDLL:
         "dflash_step_graph_destroy": ([vp], None),
         "dflash_linear": ([vp, vp, vp, i32, i32, i32, vp, vp, sz, vp], i32),
         "dflash_linear_ex": ([vp, vp, vp, i32, i32, i32, vp, i32, i32, vp, sz, vp], i32),
+        "dflash_append_kv": ([vp, vp, i64, vp, i64, vp, vp, i64, vp, vp, vp, vp, i32, vp, vp, i32,
+                              vp], i32),
         "dflash_block_attention": ([vp, vp, vp, vp, i32, i32, vp, vp, i32, vp, vp, sz, vp],
                                    i32),
         "dflash_plan_attention_info": ([i32] * 10 + [ctypes.POINTER(_AttnPlan)], i32),
@@ -201,6 +204,21 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 def _want(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
     if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+
+
+def _rows(t: torch.Tensor, shape, name: str):
+    """(pointer, row stride in elements) of a tensor [n, *shape] whose rows are
+    packed inside and any distance apart."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if tuple(t.shape[1:]) != tuple(shape):
+        raise ValueError(f"{name}: expected rows of {tuple(shape)}, got {tuple(t.shape[1:])}")
+    row = 1
+    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size > 1 and step != row:
+            raise ValueError(f"{name}: rows must be packed inside")
+        row *= size
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else row)
 
 
 def _stream(stream) -> int:
@@ -525,6 +543,43 @@ class DFlash:
                                       splits, _ptr(ws), ws.numel(), _stream(stream)),
                "dflash_linear")
         return out
+
+    def append_kv(self, k, v, positions, slot_mapping, k_cache, v_cache, k_norm=None, q=None,
+                  q_norm=None, q_out=None, stream=None) -> Optional[torch.Tensor]:
+        """Keys and values [n, Hkv, d] (and queries [n, Hq, d]) of one layer that
+        the caller projected: optional RMSNorm per head, rotation, and the paged
+        scatter (dflash_append_kv).  The rows may be slices of one fused
+        projection.  Returns the rotated queries, packed, if q is given."""
+        n, c = int(k.shape[0]), self.cfg
+        hkv, hq, d = c["n_kv_heads"] // self.tp[1], c["n_q_heads"] // self.tp[1], c["head_dim"]
+        for name, t in (("k", k), ("v", v), ("k_norm", k_norm), ("q", q), ("q_norm", q_norm),
+                        ("q_out", q_out), ("k_cache", k_cache), ("v_cache", v_cache)):
+            if t is not None:
+                _want(t, torch.bfloat16, name)
+        _want(positions, torch.int64, "positions")
+        _want(slot_mapping, torch.int64, "slot_mapping")
+        for name, t in (("v", v), ("q", q), ("positions", positions),
+                        ("slot_mapping", slot_mapping)):
+            if t is not None and int(t.shape[0]) != n:
+                raise ValueError(f"{name}: expected {n} rows")
+        for name, t in (("k_norm", k_norm), ("q_norm", q_norm)):
+            if t is not None and t.numel() != d:
+                raise ValueError(f"{name}: expected {d} values")
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            if tuple(t.shape) != (k_cache.shape[0], hkv, c.get("page_size", 16), d):
+                raise ValueError(f"{name}: expected [num_pages, {hkv}, page_size, {d}]")
+        kp, ks = _rows(k, (hkv, d), "k")
+        vp, vs = _rows(v, (hkv, d), "v")
+        qp, qs = _rows(q, (hq, d), "q") if q is not None else (None, 0)
+        if q is not None and q_out is None:
+            q_out = torch.empty(n, hq, d, dtype=torch.bfloat16, device=self.device)
+        if q_out is not None and tuple(q_out.shape) != (n, hq, d):
+            raise ValueError(f"q_out: expected [{n}, {hq}, {d}]")
+        _check(lib().dflash_append_kv(self.h, kp, ks, vp, vs, _ptr(k_norm), qp, qs, _ptr(q_norm),
+                                      _ptr(q_out), _ptr(positions), _ptr(slot_mapping), n,
+                                      _ptr(k_cache), _ptr(v_cache), int(k_cache.shape[0]),
+                                      _stream(stream)), "dflash_append_kv")
+        return q_out
 
     def block_attention(self, q, seq_lens, block_table, k_cache, v_cache, o=None,
                         workspace=None, stream=None):

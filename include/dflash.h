@@ -542,6 +542,36 @@ dflash_status dflash_linear_ex(dflash_handle* h, const void* A, const void* W, i
                                int K, float* out, int block_n, int splits, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* Keys, values and queries that the caller projected itself (a target layer, a
+ * draft layer with its own GEMMs), brought into the form the caches and the
+ * attention calls hold (§"Context KV Injection": k_norm + RoPE on keys, paged
+ * scatter), for one layer:
+ *   k' = RoPE(k_norm(k), positions)   written to k_cache at slot_mapping
+ *   v                                 written to v_cache at slot_mapping
+ *   q' = RoPE(q_norm(q), positions)   written to q_out (optional)
+ * with the handle's heads, rotation table and rms_eps; a NULL norm weight
+ * leaves the norm out.
+ *   k, v  n rows of [n_kv_heads, head_dim] bf16, rows k_stride / v_stride
+ *         ELEMENTS apart (slices of one fused projection output are fine)
+ *   q     n rows of [n_q_heads, head_dim] bf16, rows q_stride elements apart,
+ *         or NULL (then q_out and q_norm_w are NULL)
+ *   q_out [n, n_q_heads, head_dim] bf16, packed; may be q itself when q is packed
+ *   k_norm_w, q_norm_w  [head_dim] bf16, or NULL
+ *   positions, slot_mapping, k_cache, v_cache, num_pages: as
+ *         dflash_inject_context, for one layer's pools; the slots of one call
+ *         are distinct (a slot given twice holds an unspecified mix of both rows)
+ * A negative slot marks a padding row: nothing is written for it (q_out's row
+ * stays as it was).  A page outside the pool (DFLASH_DEVERR_SLOT) or a position
+ * outside the rotation table (DFLASH_DEVERR_POSITION) skips the whole row.
+ * Pointers are 16-byte aligned and strides multiples of 8 elements, at least a
+ * row long (DFLASH_ERR_INVALID_ARG otherwise).  n == 0 is a no-op.  One launch,
+ * no workspace. */
+dflash_status dflash_append_kv(dflash_handle* h, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, const void* k_norm_w, const void* q,
+                               int64_t q_stride, const void* q_norm_w, void* q_out,
+                               const int64_t* positions, const int64_t* slot_mapping, int n,
+                               void* k_cache, void* v_cache, int num_pages, void* stream);
+
 /* One layer of non-causal block attention (§"What is DFlash": every block query
  * attends to the injected context and the whole block), on a layer's caches:
  *   q [B*bs, n_q_heads, head_dim] bf16 (block rows in request order)
@@ -725,7 +755,10 @@ enum {
   DFLASH_KERNEL_GEMM_KV_INJECT = 11, /* all layers' K/V + k_norm + RoPE + scatter    */
   DFLASH_KERNEL_LINEAR = 12,         /* dflash_linear / dflash_linear_ex             */
   DFLASH_KERNEL_GEMM_MLP = 13,       /* few rows: gate/up + SwiGLU + down + residual, one launch */
-  DFLASH_KERNEL_KINDS = 14
+  DFLASH_KERNEL_APPEND_KV = 14,      /* dflash_append_kv                             */
+  DFLASH_KERNEL_PREFIX_ATTENTION = 15, /* dflash_prefix_attention: prefix and own keys */
+  DFLASH_KERNEL_PREFIX_COMBINE = 16, /* its merge of the parts                       */
+  DFLASH_KERNEL_KINDS = 17
 };
 
 /* Number of kernel launches the handle's calls have issued so far (launches

@@ -122,3 +122,9 @@ def test_create_without_device_fails_cleanly(L):
     out = ctypes.c_void_p()
     assert L.dflash_create(ctypes.byref(c), ctypes.byref(w), 0, ctypes.byref(out)) == -2
     assert out.value is None
+
+
+def test_operator_calls_validate_on_the_host(L):
+    z = None
+    assert L.dflash_append_kv(z, z, 0, z, 0, z, z, 0, z, z, z, z, 0, z, z, 1, z) == -1
+    assert D.lib().dflash_kernel_name(14).decode() == "append_kv"
