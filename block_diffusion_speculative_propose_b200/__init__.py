@@ -7,5 +7,6 @@ synthetic-input generator used by the tests and the benchmark.
 
 from .dflash import (DFlash, DFlashError, StepGraph, TargetModel, Workspace,  # noqa: F401
                      aux_capture_layers, finalize_draft_keys, lib, paged_slots,
-                     prepare_proposal_inputs, set_wait_limit, status_string, verify_greedy,
+                     prepare_proposal_inputs, sample_tokens, set_wait_limit, status_string,
+                     verify_greedy, verify_sampled, verify_sampled_workspace_bytes,
                      verify_workspace_bytes, version)

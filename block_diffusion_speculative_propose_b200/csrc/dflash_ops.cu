@@ -10,6 +10,7 @@
 #include "append_kv.cuh"
 #include "dflash.h"
 #include "handle.cuh"
+#include "sampling.cuh"
 
 namespace dflash {
 // The wait limit that this file's kernels read (see dflash_set_wait_limit).
@@ -39,6 +40,26 @@ void launch_append(dflash_handle* h, const AppendParams& p, cudaStream_t st) {
     launch_k(h->pdl, append_kv_kernel<D, 4>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
              st, p);
   }
+}
+
+// Cluster size and slice for a vocabulary: a CTA a slice of up to 8192 tokens,
+// at most eight CTAs (the portable cluster size).
+struct SamplePlan {
+  int ranks = 1, slice = 0;
+  size_t smem = 0;
+};
+SamplePlan plan_sample(int V) {
+  SamplePlan p;
+  while (p.ranks < kSmpMaxCluster && p.ranks * 8192 < V) p.ranks *= 2;
+  p.slice = (cdiv(V, p.ranks) + 3) / 4 * 4;
+  p.smem = smp_smem_bytes(p.slice);
+  return p;
+}
+
+__global__ void zero_words_kernel(unsigned* p, int n) {
+  pdl_trigger();
+  pdl_wait();
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) p[i] = 0;
 }
 
 }  // namespace
@@ -93,6 +114,89 @@ dflash_status dflash_append_kv(dflash_handle* h, const void* k, int64_t k_stride
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (c.head_dim == 128) launch_append<128>(h, p, st);
   else launch_append<64>(h, p, st);
+  return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+}
+
+dflash_status dflash_sample_tokens(const float* logits, int64_t ld, int rows, int V,
+                                   const float* temperature, const int32_t* top_k,
+                                   const float* top_p, const float* min_p, const float* u,
+                                   int32_t* tokens, float* probs, unsigned* device_error,
+                                   void* stream) {
+  if (rows < 0 || V < 1) return DFLASH_ERR_INVALID_ARG;
+  if (rows == 0) return DFLASH_OK;
+  if (!logits || !u || !tokens || ld < V || reinterpret_cast<uintptr_t>(logits) % 4)
+    return DFLASH_ERR_INVALID_ARG;
+  if (V > kSmpMaxVocab || rows > 65535) return DFLASH_ERR_UNSUPPORTED_SHAPE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dflash_status s = set_device_for(st, tokens);
+  if (s != DFLASH_OK) return s;
+  const SamplePlan pl = plan_sample(V);
+  SampleParams p;
+  p.logits = logits;
+  p.ld = ld;
+  p.rows = rows;
+  p.V = V;
+  p.slice = pl.slice;
+  p.set = {temperature, top_k, top_p, min_p};
+  p.u = u;
+  p.tokens = tokens;
+  p.probs = probs;
+  p.err = device_error;
+  DF_CUDA(cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(pl.smem)));
+  launch_kc(pdl_default(), pl.ranks, sample_kernel, dim3(pl.ranks, rows), dim3(kSmpThreads),
+            pl.smem, st, p);
+  return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+}
+
+size_t dflash_verify_sampled_workspace_bytes(int B, int K) {
+  if (B <= 0 || K < 0) return 0;
+  return align_up(static_cast<size_t>(B) * (K + 3) * 4);
+}
+
+dflash_status dflash_verify_sampled(const int32_t* drafts, const float* target_logits, int64_t ld,
+                                    int B, int K, int V, const float* temperature,
+                                    const int32_t* top_k, const float* top_p, const float* min_p,
+                                    const float* u_accept, const float* u_sample,
+                                    int32_t* out_tokens, int32_t* num_accepted, int32_t* bonus,
+                                    unsigned* device_error, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  if (B < 0 || K < 0 || V < 1 || K > 128) return DFLASH_ERR_INVALID_ARG;
+  if (B == 0) return DFLASH_OK;
+  if ((K > 0 && (!drafts || !u_accept)) || !target_logits || !u_sample || !out_tokens ||
+      !num_accepted || !bonus || !workspace || ld < V ||
+      reinterpret_cast<uintptr_t>(target_logits) % 4 || reinterpret_cast<uintptr_t>(workspace) % 4)
+    return DFLASH_ERR_INVALID_ARG;
+  if (V > kSmpMaxVocab || B > 65535) return DFLASH_ERR_UNSUPPORTED_SHAPE;
+  if (workspace_bytes < dflash_verify_sampled_workspace_bytes(B, K)) return DFLASH_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dflash_status s = set_device_for(st, out_tokens);
+  if (s != DFLASH_OK) return s;
+  const SamplePlan pl = plan_sample(V);
+  VerifySampledParams p;
+  p.drafts = drafts;
+  p.logits = target_logits;
+  p.ld = ld;
+  p.B = B;
+  p.K = K;
+  p.V = V;
+  p.slice = pl.slice;
+  p.set = {temperature, top_k, top_p, min_p};
+  p.u_accept = u_accept;
+  p.u_sample = u_sample;
+  p.out = out_tokens;
+  p.num_accepted = num_accepted;
+  p.bonus = bonus;
+  p.err = device_error;
+  p.done = static_cast<unsigned*>(workspace);
+  p.refused = p.done + B;
+  p.row_token = static_cast<int32_t*>(workspace) + 2 * static_cast<int64_t>(B);
+  DF_CUDA(cudaFuncSetAttribute(verify_sampled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(pl.smem)));
+  launch_k(pdl_default(), zero_words_kernel, dim3(std::min(cdiv(2 * B, 256), 64)), dim3(256), 0,
+           st, p.done, 2 * B);
+  launch_kc(pdl_default(), pl.ranks, verify_sampled_kernel, dim3(pl.ranks, B, K + 1),
+            dim3(kSmpThreads), pl.smem, st, p);
   return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 

@@ -155,6 +155,9 @@ def lib() -> ctypes.CDLL:
         "dflash_finalize_draft_keys": ([vp, vp, i32, i32, i32, vp, vp, vp, vp], i32),
         "dflash_verify_greedy": ([vp, vp, i32, i32, i32, vp, vp, vp, vp, sz, vp], i32),
         "dflash_verify_greedy_noalloc": ([vp, vp, i32, i32, i32, vp, vp, vp, vp], i32),
+        "dflash_sample_tokens": ([vp, i64, i32, i32] + [vp] * 9, i32),
+        "dflash_verify_sampled_workspace_bytes": ([i32, i32], sz),
+        "dflash_verify_sampled": ([vp, vp, i64, i32, i32, i32] + [vp] * 11 + [sz, vp], i32),
         "dflash_spec_step_workspace_bytes": ([vp, i32, i32, i32], sz),
         "dflash_spec_step": ([vp, ctypes.POINTER(_StepIO), vp, sz, vp], i32),
         "dflash_step_graph_create": ([vp, ctypes.POINTER(_StepIO), vp, sz, ctypes.POINTER(vp)],
@@ -848,6 +851,93 @@ def verify_greedy_noalloc(drafts, target_logits, out_tokens=None, num_accepted=N
                                               _ptr(out_tokens), _ptr(num_accepted), _ptr(bonus),
                                               _stream(stream)),
            "dflash_verify_greedy_noalloc")
+    return out_tokens, num_accepted, bonus
+
+
+def _settings(n: int, temperature, top_k, top_p, min_p):
+    """Pointers of the per-row sampling settings, each checked for type and length."""
+    out = []
+    for name, t, dt in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if t is not None:
+            _want(t, dt, name)
+            if t.numel() != n:
+                raise ValueError(f"{name}: expected {n} values")
+        out.append(_ptr(t))
+    return out
+
+
+def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None,
+                  probs=None, return_probs: bool = False, device_error=None, stream=None):
+    """One token per row of ``logits`` [rows, V] fp32 (rows any distance apart)
+    from the uniform numbers ``u`` [rows] (dflash_sample_tokens); the settings
+    are per-row tensors or None.  Returns the tokens [rows] int32, with
+    ``return_probs`` (or ``probs``) the pair (tokens, probabilities)."""
+    _want(logits, torch.float32, "logits")
+    _want(u, torch.float32, "u")
+    rows, V = logits.shape
+    ptr, ld = _rows(logits, (V,), "logits")
+    if u.numel() != rows:
+        raise ValueError(f"u: expected {rows} values")
+    if tokens is None:
+        tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
+    if probs is None and return_probs:
+        probs = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    _want(tokens, torch.int32, "tokens")
+    if probs is not None:
+        _want(probs, torch.float32, "probs")
+    if tokens.numel() != rows or (probs is not None and probs.numel() != rows):
+        raise ValueError(f"tokens, probs: expected {rows} values")
+    _check(lib().dflash_sample_tokens(ptr, ld, rows, V,
+                                      *_settings(rows, temperature, top_k, top_p, min_p), _ptr(u),
+                                      _ptr(tokens), _ptr(probs), _ptr(device_error),
+                                      _stream(stream)), "dflash_sample_tokens")
+    return tokens if probs is None else (tokens, probs)
+
+
+def verify_sampled_workspace_bytes(B: int, K: int) -> int:
+    return lib().dflash_verify_sampled_workspace_bytes(B, K)
+
+
+def verify_sampled(drafts, target_logits, u_accept, u_sample, temperature=None, top_k=None,
+                   top_p=None, min_p=None, out_tokens=None, num_accepted=None, bonus=None,
+                   device_error=None, workspace=None, stream=None):
+    """Acceptance of greedy drafts [B, K] against a sampling target
+    (dflash_verify_sampled): ``u_accept`` [B, K] and ``u_sample`` [B] are uniform
+    numbers, the settings [B] tensors or None.  Returns (out_tokens, n, bonus),
+    as verify_greedy."""
+    _want(drafts, torch.int32, "drafts")
+    _want(target_logits, torch.float32, "target_logits")
+    _want(u_accept, torch.float32, "u_accept")
+    _want(u_sample, torch.float32, "u_sample")
+    B, K1, V = target_logits.shape
+    K, dev = K1 - 1, target_logits.device
+    if tuple(drafts.shape) != (B, K) or tuple(u_accept.shape) != (B, K) or u_sample.numel() != B:
+        raise ValueError(f"expected drafts and u_accept [{B}, {K}] and u_sample [{B}]")
+    ptr, ld = _rows(target_logits.flatten(0, 1) if B * K1 else target_logits[:, 0], (V,),
+                    "target_logits")
+    if ptr != target_logits.data_ptr():
+        raise ValueError("target_logits: rows must be equally far apart")
+    if out_tokens is None:
+        out_tokens = torch.empty(B, K1, dtype=torch.int32, device=dev)
+    if num_accepted is None:
+        num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+    if bonus is None:
+        bonus = torch.empty(B, dtype=torch.int32, device=dev)
+    for name, t, n in (("out_tokens", out_tokens, B * K1), ("num_accepted", num_accepted, B),
+                       ("bonus", bonus, B)):
+        _want(t, torch.int32, name)
+        if t.numel() != n:
+            raise ValueError(f"{name}: expected {n} values")
+    if workspace is None:
+        workspace = torch.empty(max(verify_sampled_workspace_bytes(B, K), 256), dtype=torch.uint8,
+                                device=dev)
+    _check(lib().dflash_verify_sampled(_ptr(drafts), ptr, ld, B, K, V,
+                                       *_settings(B, temperature, top_k, top_p, min_p),
+                                       _ptr(u_accept), _ptr(u_sample), _ptr(out_tokens),
+                                       _ptr(num_accepted), _ptr(bonus), _ptr(device_error),
+                                       _ptr(workspace), workspace.numel(), _stream(stream)),
+           "dflash_verify_sampled")
     return out_tokens, num_accepted, bonus
 
 

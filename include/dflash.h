@@ -418,6 +418,70 @@ dflash_status dflash_verify_greedy(const int32_t* drafts, const float* target_lo
                                    void* workspace, size_t workspace_bytes,
                                    void* stream);
 
+/* ---- sampling (temperature > 0) ------------------------------------------
+ *
+ * The pages decode greedily; these calls are the same two steps for a target
+ * that samples, an addition of this library.
+ *
+ * Per-row settings, each a DEVICE array of one entry per row (per request for
+ * dflash_verify_sampled) or NULL:
+ *   temperature  NULL: 1; <= 0 or NaN: greedy (the largest logit, ties -> lowest id)
+ *   top_k        NULL or <= 0: off
+ *   min_p        NULL or <= 0: off; relative to the largest probability, above 1 as 1
+ *   top_p        NULL or >= 1: off; <= 0 keeps the largest logit alone
+ * A token with logit x weighs exp((x - max) / temperature) (NaN and -inf weigh
+ * nothing; where the largest logit is +inf, the +inf ones share the row).
+ * In falling order (ties -> lowest id first) the first top_k tokens are kept,
+ * of these the ones that weigh at least min_p times the largest, and of these
+ * the shortest run from the top whose weight reaches top_p of theirs; the
+ * largest is always kept.  A draw with u is the first token in vocabulary order
+ * whose running sum of kept weights exceeds u times their sum; u is clamped
+ * into [0, 1), NaN counts as 0.  Weights are held to 2^-45 of the largest and
+ * summed exactly: the result depends on no order of additions. */
+
+/* One token for each of `rows` rows of logits, [rows, V] fp32 with rows ld >= V
+ * elements apart (any 4-byte alignment; 16-byte aligned rows load faster).
+ *   u      [rows] fp32, uniform in [0, 1)
+ *   tokens [rows] int32 out; -1 where a row holds nothing but -inf and NaN
+ *          (sets DFLASH_DEVERR_INPUT in *device_error, a nullable device word)
+ *   probs  [rows] fp32 out, the token's probability among the kept ones (0 for
+ *          -1, 1 for greedy rows); may be NULL
+ * rows == 0 is a no-op; V > 393216 or rows > 65535 is
+ * DFLASH_ERR_UNSUPPORTED_SHAPE.  One launch, no workspace. */
+dflash_status dflash_sample_tokens(const float* logits, int64_t ld, int rows, int V,
+                                   const float* temperature, const int32_t* top_k,
+                                   const float* top_p, const float* min_p, const float* u,
+                                   int32_t* tokens, float* probs, unsigned* device_error,
+                                   void* stream);
+
+/* Verification of greedy drafts against a target that samples: the emitted
+ * tokens are distributed as if the target had sampled every one.  With p_j the
+ * filtered distribution of target_logits row j (row meaning as for
+ * dflash_verify_greedy; the draft proposes its argmax, so its own distribution
+ * is one at drafts[b][j]):
+ *   n = the first j < K with u_accept[b][j] >= p_j(drafts[b][j]), else K
+ *   t = a draw with u_sample[b] from p_n, for n < K without drafts[b][n]
+ *   out_tokens[b] = [drafts[b][0..n-1], t, -1, ..., -1], num_accepted[b] = n,
+ *   bonus[b] = t
+ * the outputs of dflash_verify_greedy, as dflash_prepare_proposal_inputs takes
+ * them; a greedy row (temperature <= 0) decides as dflash_verify_greedy does.
+ * A draft that holds all the kept probability is accepted whatever u_accept; a
+ * draft outside [0, V) is refused.  Where row n holds nothing but -inf and NaN,
+ * t = -1 and DFLASH_DEVERR_INPUT is set in *device_error (nullable).
+ *   drafts, u_accept [B, K]; u_sample [B]; target_logits [B, K+1, V] fp32, rows
+ *   ld >= V elements apart; settings [B].
+ * B == 0 is a no-op; V > 393216 or B > 65535 is DFLASH_ERR_UNSUPPORTED_SHAPE,
+ * K > 128 DFLASH_ERR_INVALID_ARG.  Needs
+ * dflash_verify_sampled_workspace_bytes(B, K) of 4-byte aligned workspace. */
+size_t dflash_verify_sampled_workspace_bytes(int B, int K);
+dflash_status dflash_verify_sampled(const int32_t* drafts, const float* target_logits, int64_t ld,
+                                    int B, int K, int V, const float* temperature,
+                                    const int32_t* top_k, const float* top_p, const float* min_p,
+                                    const float* u_accept, const float* u_sample,
+                                    int32_t* out_tokens, int32_t* num_accepted, int32_t* bonus,
+                                    unsigned* device_error, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 /* ---- the whole speculative step ------------------------------------------ */
 
 /* Buffers of one speculative-decoding step (dflash_spec_step).  Device

@@ -128,3 +128,20 @@ def test_operator_calls_validate_on_the_host(L):
     z = None
     assert L.dflash_append_kv(z, z, 0, z, 0, z, z, 0, z, z, z, z, 0, z, z, 1, z) == -1
     assert D.lib().dflash_kernel_name(14).decode() == "append_kv"
+    one = ctypes.c_void_p(16)
+    f = L.dflash_sample_tokens
+    assert f(z, 10, -1, 10, z, z, z, z, z, z, z, z, z) == -1
+    assert f(z, 10, 0, 10, z, z, z, z, z, z, z, z, z) == 0
+    assert f(z, 10, 1, 10, z, z, z, z, one, one, z, z, z) == -1        # no logits
+    assert f(one, 9, 1, 10, z, z, z, z, one, one, z, z, z) == -1       # rows overlap
+    assert f(one, 10, 1, 0, z, z, z, z, one, one, z, z, z) == -1
+    assert f(ctypes.c_void_p(18), 10, 1, 10, z, z, z, z, one, one, z, z, z) == -1
+    assert f(one, 400000, 1, 400000, z, z, z, z, one, one, z, z, z) == -4
+    assert f(one, 10, 65536, 10, z, z, z, z, one, one, z, z, z) == -4
+    f = L.dflash_verify_sampled
+    assert f(z, z, 10, 0, 3, 10, z, z, z, z, z, z, z, z, z, z, z, 0, z) == 0
+    assert f(z, z, 10, 2, 129, 10, z, z, z, z, z, z, z, z, z, z, z, 0, z) == -1
+    assert f(z, one, 10, 2, 3, 10, z, z, z, z, one, one, one, one, one, z, one, 999, z) == -1
+    assert f(one, one, 10, 2, 3, 10, z, z, z, z, one, one, one, one, one, z, one, 8, z) == -3
+    assert L.dflash_verify_sampled_workspace_bytes(2, 3) >= 2 * 6 * 4
+    assert L.dflash_verify_sampled_workspace_bytes(0, 3) == 0
