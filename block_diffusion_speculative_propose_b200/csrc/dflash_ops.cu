@@ -10,6 +10,7 @@
 #include "append_kv.cuh"
 #include "dflash.h"
 #include "handle.cuh"
+#include "prefix_attention.cuh"
 #include "sampling.cuh"
 
 namespace dflash {
@@ -54,6 +55,113 @@ SamplePlan plan_sample(int V) {
   p.slice = (cdiv(V, p.ranks) + 3) / 4 * 4;
   p.smem = smp_smem_bytes(p.slice);
   return p;
+}
+
+// Attention over a shared prefix: which kernel takes the prefix, how it is
+// dealt, the splits of the requests' own keys, and the workspace.
+struct PrefixPlan {
+  int nt = 1, kt = 64;           // the prefix's kernel
+  int tpt = 0, row_groups = 0, items = 0, tiles = 0, ctas = 0, max_segs = 0;
+  int chunk = 0, splits = 0, R = 0;
+  size_t off_ml = 0, off_own = 0, off_own_ml = 0, total = 0;
+};
+PrefixPlan plan_prefix(const dflash_handle* h, int B, int q_len, int W, int prefix_pages) {
+  const dflash_config& c = h->cfg;
+  const int G = c.n_q_heads / c.n_kv_heads, Hkv = c.n_kv_heads, D = c.head_dim;
+  PrefixPlan p;
+  p.R = q_len * G;
+  p.tpt = 128 / G;
+  const int row_tiles = cdiv(B * q_len, p.tpt);
+  if (prefix_pages > 0) {
+    // One row tile: the prefix is a stream like the requests' own keys.  More:
+    // two tiles share each key tile.
+    p.nt = row_tiles > 1 ? 2 : 1;
+    p.kt = p.nt == 2 ? 128 : 64;
+    p.row_groups = cdiv(row_tiles, p.nt);
+    p.items = Hkv * p.row_groups;
+    p.tiles = cdiv(prefix_pages * 16, p.kt);
+    const int64_t units = static_cast<int64_t>(p.items) * p.tiles;
+    const int slots = p.nt == 2 ? h->num_sms : 2 * h->num_sms;
+    p.ctas = static_cast<int>(std::min<int64_t>(slots, (units + 1) / 2));
+    const int64_t longest = (units + p.ctas - 1) / p.ctas;
+    p.max_segs = static_cast<int>((longest - 1) / p.tiles + 2);
+  }
+  const int own_keys = (W - prefix_pages) * 16;
+  if (own_keys > 0) {
+    const double est = static_cast<double>(B) * Hkv * own_keys;
+    int chunk = static_cast<int>(std::ceil(est / (8.0 * h->num_sms)));
+    chunk = std::max(128, std::min(8192, (chunk + 63) / 64 * 64));
+    p.chunk = chunk;
+    p.splits = cdiv(own_keys, chunk);
+  }
+  const size_t pr = static_cast<size_t>(p.ctas) * p.max_segs * p.nt * 128;
+  const size_t ow = static_cast<size_t>(p.splits) * B * Hkv * p.R;
+  p.off_ml = align_up(pr * D * 4);
+  p.off_own = p.off_ml + align_up(pr * 8);
+  p.off_own_ml = p.off_own + align_up(ow * D * 4);
+  p.total = p.off_own_ml + align_up(ow * 8) + kAlign;
+  return p;
+}
+
+template <int D, int NT, int KT>
+dflash_status launch_part(dflash_handle* h, const CUtensorMap& tq, const CUtensorMap& tk,
+                          const CUtensorMap& tv, const PartParams& p, int64_t ctas,
+                          cudaStream_t st) {
+  using C = PartCfg<D, NT, KT>;
+  DF_CUDA(cudaFuncSetAttribute(attn_part_kernel<D, NT, KT>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+  LaunchScope scope(h, DFLASH_KERNEL_PREFIX_ATTENTION, st);
+  launch_k(h->pdl, attn_part_kernel<D, NT, KT>, dim3(static_cast<unsigned>(ctas)),
+           dim3(C::kThreads), C::kSmem, st, tq, tk, tv, p);
+  return DFLASH_OK;
+}
+
+// Query tokens [n_tok][Hq][D] in boxes of tpt tokens x G heads x 64 columns.
+bool make_q_map(CUtensorMap* map, const void* q, int n_tok, int Hq, int D, int G, int tpt) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
+                        static_cast<cuuint64_t>(n_tok)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hq) * D * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tpt)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+dflash_status run_prefix(dflash_handle* h, const PrefixPlan& pl, PartParams p, const void* q,
+                         const void* kc, const void* vc, f16* o, cudaStream_t st) {
+  CUtensorMap tq, tk, tv;
+  const uint64_t rows = static_cast<uint64_t>(p.num_pages) * p.Hkv * 16;
+  if (!make_q_map(&tq, q, p.n_tok, p.Hq, D, p.G, p.tpt) || !h->tmap(&tk, kc, rows, D, 16) ||
+      !h->tmap(&tv, vc, rows, D, 16))
+    return DFLASH_ERR_CUDA;
+  dflash_status s = DFLASH_OK;
+  PartParams own = p;
+  if (pl.nt == 2) {
+    s = launch_part<D, 2, 128>(h, tq, tk, tv, p, pl.ctas, st);
+    own.prefix_ctas = 0;
+  }
+  const int64_t ctas = own.prefix_ctas + static_cast<int64_t>(pl.splits) * p.B * p.Hkv;
+  if (s == DFLASH_OK && ctas > 0) s = launch_part<D, 1, 64>(h, tq, tk, tv, own, ctas, st);
+  if (s != DFLASH_OK) return s;
+  LaunchScope scope(h, DFLASH_KERNEL_PREFIX_COMBINE, st);
+  launch_k(h->pdl, attn_join_kernel<D>, dim3(static_cast<unsigned>(
+               (static_cast<int64_t>(p.n_tok) * p.Hq + 7) / 8)), dim3(256), 0, st, p, pl.nt, o);
+  return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+}
+
+// Geometry of a prefix-attention call: OK or what is wrong with it.
+dflash_status check_prefix(const dflash_handle* h, int B, int q_len, int W, int prefix_pages) {
+  if (!h || B < 0 || q_len < 1 || W < 1 || prefix_pages < 0 || prefix_pages > W)
+    return DFLASH_ERR_INVALID_ARG;
+  const int G = h->cfg.n_q_heads / h->cfg.n_kv_heads;
+  if (B > 65535 || q_len * static_cast<int64_t>(G) > 128 || W > (1 << 24))
+    return DFLASH_ERR_UNSUPPORTED_SHAPE;
+  return DFLASH_OK;
 }
 
 __global__ void zero_words_kernel(unsigned* p, int n) {
@@ -115,6 +223,66 @@ dflash_status dflash_append_kv(dflash_handle* h, const void* k, int64_t k_stride
   if (c.head_dim == 128) launch_append<128>(h, p, st);
   else launch_append<64>(h, p, st);
   return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+}
+
+size_t dflash_prefix_attention_workspace_bytes(const dflash_handle* h, int B, int q_len,
+                                               int max_pages_per_seq, int prefix_pages) {
+  if (check_prefix(h, B, q_len, max_pages_per_seq, prefix_pages) != DFLASH_OK || B == 0) return 0;
+  return plan_prefix(h, B, q_len, max_pages_per_seq, prefix_pages).total;
+}
+
+dflash_status dflash_prefix_attention(dflash_handle* h, const void* q, int q_len, int causal,
+                                      const int32_t* seq_lens, const int32_t* block_table, int B,
+                                      int max_pages_per_seq, int prefix_pages,
+                                      const void* k_cache, const void* v_cache, int num_pages,
+                                      void* o, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  const dflash_status s = check_prefix(h, B, q_len, max_pages_per_seq, prefix_pages);
+  if (s != DFLASH_OK || B == 0) return s;
+  if (!q || !seq_lens || !block_table || !k_cache || !v_cache || num_pages < 1 || !o ||
+      !workspace || !aligned16(q) || !aligned16(o) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      reinterpret_cast<uintptr_t>(workspace) % kAlign)
+    return DFLASH_ERR_INVALID_ARG;
+  const dflash_config& c = h->cfg;
+  if (static_cast<int64_t>(num_pages) * c.n_kv_heads * 16 > INT32_MAX)
+    return DFLASH_ERR_UNSUPPORTED_SHAPE;   // rows of the pools' tensor maps
+  const PrefixPlan pl = plan_prefix(h, B, q_len, max_pages_per_seq, prefix_pages);
+  if (workspace_bytes < pl.total) return DFLASH_ERR_WORKSPACE;
+  DF_CUDA(use_device(h->device));
+  PartParams p;
+  p.B = B;
+  p.q_len = q_len;
+  p.n_tok = B * q_len;
+  p.Hq = c.n_q_heads;
+  p.Hkv = c.n_kv_heads;
+  p.G = c.n_q_heads / c.n_kv_heads;
+  p.tpt = pl.tpt;
+  p.causal = causal ? 1 : 0;
+  p.seq_lens = seq_lens;
+  p.block_table = block_table;
+  p.W = max_pages_per_seq;
+  p.num_pages = num_pages;
+  p.prefix_keys = prefix_pages * 16;
+  p.prefix_ctas = pl.ctas;
+  p.prefix_items = pl.items;
+  p.prefix_tiles = pl.tiles;
+  p.row_groups = pl.row_groups;
+  p.max_segs = pl.max_segs;
+  p.prefix_o = at<float>(workspace, 0);
+  p.prefix_ml = at<float2>(workspace, pl.off_ml);
+  p.chunk_keys = pl.chunk;
+  p.max_splits = pl.splits;
+  p.R = pl.R;
+  p.own_o = at<float>(workspace, pl.off_own);
+  p.own_ml = at<float2>(workspace, pl.off_own_ml);
+  p.scale_log2 =
+      static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c.head_dim)));
+  p.err = h->dev_err;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return c.head_dim == 128 ? run_prefix<128>(h, pl, p, q, k_cache, v_cache,
+                                             static_cast<f16*>(o), st)
+                           : run_prefix<64>(h, pl, p, q, k_cache, v_cache, static_cast<f16*>(o),
+                                            st);
 }
 
 dflash_status dflash_sample_tokens(const float* logits, int64_t ld, int rows, int V,

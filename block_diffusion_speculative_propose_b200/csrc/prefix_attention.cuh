@@ -1,0 +1,553 @@
+// prefix_attention.cuh — attention of a batch of query blocks whose requests
+// share their first pages.
+//
+// o = softmax(q K^T / sqrt(D)) V over the keys of a row is a sum over parts of
+// them: with a reference m, l = sum 2^(s - m) and O = sum 2^(s - m) v of each
+// part (s in units of log2), the whole is sum 2^(m - M) O / sum 2^(m - M) l.
+// So the shared prefix is one dense attention of every row of the batch against
+// keys that are read once, each request's own keys are another, and a merge
+// joins them.
+//   prefix   bound by the tensor cores: 4 D flops a row and key, the keys read
+//            once per 256 rows from L2
+//   own keys bound by HBM: 4 D bytes a key and kv head
+//
+// attn_part_kernel<D, NT, KT> runs both.  NT row tiles of 128 query rows share
+// the K/V tiles of KT keys that pass through a ring in shared memory; S and,
+// in its place, P (bf16) stay in tensor memory beside O:
+//   warp 0      TMA producer: lane j loads page j % (KT / 16), column half j / ..
+//   warp 1      MMA issuer (one thread): S_i = Q_i K^T, O_i += P_i V with P_i
+//               read from tensor memory
+//   then 4 warps for each row tile: thread = row, so the maximum, the sum and
+//               the mask of a row need no exchange
+// The issue order PV_0(t) S_0(t+1) PV_1(t) S_1(t+1) keeps the tensor cores on one
+// tile while the other one's softmax runs (NT = 2); with NT = 1 two CTAs an SM
+// do the same for one another.
+//   NT = 2, KT = 128: one CTA an SM, 4 D x 128 flops per byte read, for many rows
+//   NT = 1, KT = 64:  two CTAs an SM, for one request's rows
+#pragma once
+
+#include "dflash_device.cuh"
+
+namespace dflash {
+
+constexpr float kPartHeadroom = 32.f;   // log2 of the largest 2^(s - m) kept unscaled
+
+struct PartParams {
+  // query tokens [n_tok = B * q_len][Hq][D]; row r of a tile that starts at
+  // token t: token t + r / G, query head h * G + r % G
+  int B, q_len, n_tok, Hq, Hkv, G, tpt;   // tpt = 128 / G tokens a tile
+  int causal;
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  int W, num_pages, prefix_keys;
+  // the prefix, dealt to the first prefix_ctas CTAs in equal runs of
+  // (item = kv head and row tiles, key tile)
+  int prefix_ctas, prefix_items, prefix_tiles, row_groups;   // row_groups = items per kv head
+  int max_segs;
+  float* prefix_o;     // [prefix_ctas][max_segs][NT][128][D]
+  float2* prefix_ml;   // [prefix_ctas][max_segs][NT][128]
+  // own keys: one CTA per (split, request, kv head)
+  int chunk_keys, max_splits, R;          // R = q_len * G
+  float* own_o;        // [max_splits][B][Hkv][R][D]
+  float2* own_ml;      // [max_splits][B][Hkv][R]
+  float scale_log2;
+  unsigned* err;
+};
+
+template <int D_, int NT_, int KT_>
+struct PartCfg {
+  static constexpr int D = D_, NT = NT_, KT = KT_;
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTileBytes = KT * D * 2;
+  static constexpr int kQBytes = 128 * D * 2;
+  static constexpr int kCtas = NT == 1 ? 2 : 1;            // per SM
+  static constexpr int kRoom = 232448 / kCtas - 2048;
+  static constexpr int kFit = (kRoom - NT * kQBytes) / kTileBytes;
+  static constexpr int NS = kFit > 6 ? 6 : kFit;           // ring slots (K or V tiles)
+  static constexpr int kOffRing = NT * kQBytes;
+  static constexpr int kOffBar = kOffRing + NS * kTileBytes;
+  static constexpr int kSmem = 1024 + kOffBar + 256;
+  static constexpr int kThreads = 64 + NT * 128;
+  static constexpr int kCols = NT * (KT + D) > 256 ? 512 : NT * (KT + D) > 128 ? 256 : 128;
+  static_assert(NS >= 3, "ring");
+  static_assert(kCols * kCtas <= 512, "tensor memory");
+};
+
+__device__ __forceinline__ float part_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void part_fence_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void part_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                             int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, A: 128 lanes x packed pairs.
+__device__ __forceinline__ void part_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void part_st_x32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// kind::f16, bf16 x bf16 -> fp32; b_mn: B is MN-major.
+__host__ __device__ constexpr uint32_t part_idesc(int M, int N, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// One run of key tiles for one set of row tiles.
+struct PartSeg {
+  int h, tok0, b;      // b: whose table row and own keys; -1: the prefix
+  int key0, key1;      // absolute keys, key0 a multiple of 16
+  int n_tiles;
+  int slot;            // partial result
+};
+
+// First (item, tile) unit of prefix CTA c, of `units` in all.
+__host__ __device__ __forceinline__ long long part_begin(long long units, int ctas, int c) {
+  return units * c / ctas;
+}
+
+template <int NT, int KT>
+__device__ __forceinline__ bool part_segment(const PartParams& p, int k, PartSeg& s) {
+  if (static_cast<int>(blockIdx.x) < p.prefix_ctas) {
+    const long long units = static_cast<long long>(p.prefix_items) * p.prefix_tiles;
+    const long long u0 = part_begin(units, p.prefix_ctas, blockIdx.x);
+    const long long u1 = part_begin(units, p.prefix_ctas, blockIdx.x + 1);
+    const int item0 = static_cast<int>(u0 / p.prefix_tiles);
+    const int item = item0 + k;
+    const long long a = max(u0, static_cast<long long>(item) * p.prefix_tiles);
+    const long long e = min(u1, static_cast<long long>(item + 1) * p.prefix_tiles);
+    if (a >= e || k >= p.max_segs) return false;
+    const int t0 = static_cast<int>(a - static_cast<long long>(item) * p.prefix_tiles);
+    s.n_tiles = static_cast<int>(e - a);
+    s.h = item / p.row_groups;
+    s.tok0 = (item - s.h * p.row_groups) * NT * p.tpt;
+    s.b = -1;
+    s.key0 = t0 * KT;
+    s.key1 = min(p.prefix_keys, (t0 + s.n_tiles) * KT);
+    s.slot = blockIdx.x * p.max_segs + k;
+    return true;
+  }
+  if (k > 0) return false;
+  int i = static_cast<int>(blockIdx.x) - p.prefix_ctas;
+  s.h = i % p.Hkv;
+  i /= p.Hkv;
+  s.b = i % p.B;
+  const int split = i / p.B;
+  const int seq = p.seq_lens[s.b];
+  s.key0 = p.prefix_keys + split * p.chunk_keys;
+  // 64-bit: seq may be anything
+  s.key1 = seq < 0 ? 0
+                   : static_cast<int>(min(static_cast<long long>(seq) + p.q_len,
+                                          static_cast<long long>(s.key0) + p.chunk_keys));
+  if (s.key0 >= s.key1) return false;
+  s.n_tiles = (s.key1 - s.key0 + KT - 1) / KT;
+  s.tok0 = s.b * p.q_len;
+  s.slot = (split * p.B + s.b) * p.Hkv + s.h;
+  return true;
+}
+
+template <int D, int NT, int KT>
+__global__ void __launch_bounds__(64 + NT * 128, NT == 1 ? 2 : 1)
+attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const PartParams p) {
+  using C = PartCfg<D, NT, KT>;
+  constexpr int NS = C::NS, kHalves = C::kHalves;
+  pdl_trigger();
+  pdl_wait();
+  PartSeg seg;
+  if (!part_segment<NT, KT>(p, 0, seg)) return;   // the same for the whole CTA
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  extern __shared__ uint8_t part_smem[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(part_smem) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* full = bars;             // [NS] a K or V tile has landed
+  uint64_t* empty = bars + 8;        // [NS] its last MMA has run
+  uint64_t* q_full = bars + 16;
+  uint64_t* q_empty = bars + 17;     // the segment's last S has run
+  uint64_t* s_full = bars + 18;      // [NT] S of a tile is there (and P V of the one before)
+  uint64_t* p_full = bars + 20;      // [NT] P of a tile is written
+  uint64_t* o_full = bars + 22;      // [NT] the segment's last P V has run
+  uint64_t* o_free = bars + 24;      // [NT] O has been read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
+  auto ring = [&](int s) { return smem + C::kOffRing + s * C::kTileBytes; };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < NT; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_free[i], 4);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  cta_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto col_s = [&](int i) { return tmem + i * KT; };
+  auto col_o = [&](int i) { return tmem + NT * KT + i * D; };
+  // The ring holds K_0, then K_(t+1), V_t for each t: the order of use.
+  // K_t is tile 2t - 1 of its segment (K_0: 0), V_t tile 2t + 2 (the last: 2t + 1).
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    constexpr int kPages = KT / 16;
+    const int pj = lane % kPages, half = lane / kPages;
+    const bool loads = lane < kPages * kHalves;
+    unsigned seq = 0;      // ring tiles issued
+    bool ok = true;
+    for (int k = 0; ok && part_segment<NT, KT>(p, k, seg); ++k) {
+      if (lane == 0) {
+        ok = mbar_wait(q_empty, (k & 1) ^ 1u, p.err);
+        if (ok) {
+          mbar_arrive_expect_tx(q_full, NT * kHalves * p.tpt * p.G * 128);
+          for (int i = 0; i < NT; ++i)
+            for (int hf = 0; hf < kHalves; ++hf)
+              part_load_3d(smem + (i * kHalves + hf) * 128 * 128, &tmQ, q_full, hf * 64,
+                           seg.h * p.G, seg.tok0 + i * p.tpt);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      const int32_t* table = p.block_table + static_cast<size_t>(max(seg.b, 0)) * p.W;
+      // row of the pools' [pages * Hkv * 16, D] view where this lane's page of
+      // tile t starts; -16 (zeros are filled in) past the range, the table or the pool
+      auto page_row = [&](int t) {
+        const int key = seg.key0 + t * KT + pj * 16;
+        if (t >= seg.n_tiles || key >= seg.key1) return -16;
+        const int pg = key >> 4;
+        if (pg >= p.W) {
+          raise_error(p.err, DFLASH_DEVERR_TABLE);
+          return -16;
+        }
+        const int page = table[pg];
+        if (page < 0 || page >= p.num_pages) {
+          raise_error(p.err, DFLASH_DEVERR_SLOT);
+          return -16;
+        }
+        return (page * p.Hkv + seg.h) * 16;
+      };
+      auto issue = [&](const CUtensorMap* map, int row) {
+        const int s = seq % NS;
+        if (lane == 0) {
+          ok = mbar_wait(&empty[s], ((seq / NS) & 1) ^ 1u, p.err);
+          if (ok) mbar_arrive_expect_tx(&full[s], C::kTileBytes);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        __syncwarp();
+        if (ok && loads)
+          tma_load_2d(ring(s) + half * KT * 128 + pj * 2048, map, &full[s], half * 64, row);
+        ++seq;
+      };
+      int row = page_row(0), next = page_row(1);
+      if (ok) issue(&tmK, row);
+      for (int t = 0; ok && t < seg.n_tiles; ++t) {
+        const int after = page_row(t + 2);
+        if (t + 1 < seg.n_tiles) issue(&tmK, next);
+        if (ok) issue(&tmV, row);
+        row = next;
+        next = after;
+      }
+    }
+    if (!ok && lane == 0) {
+      // given up: let the copies in flight land before the CTA's memory goes
+      for (unsigned s = seq > NS ? seq - NS : 0; s < seq; ++s)
+        for (int spin = 0; spin < 100000 && !mbar_test_wait(&full[s % NS], (s / NS) & 1); ++spin) {
+        }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id_s = part_idesc(128, KT, false);
+      constexpr uint32_t id_o = part_idesc(128, D, true);
+      unsigned seq = 0;
+      unsigned tiles = 0;      // key tiles done before this segment
+      bool ok = true;
+      auto mma_s = [&](int i, int s) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int hf = kk >> 2, w = kk & 3;
+          umma_f16kind(col_s(i),
+                       umma_desc_sw128(smem_u32(smem + (i * kHalves + hf) * 128 * 128 + w * 32)),
+                       umma_desc_sw128(smem_u32(ring(s) + hf * KT * 128 + w * 32)), id_s,
+                       kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[i]);
+      };
+      auto landed = [&](unsigned n) { return mbar_wait(&full[n % NS], (n / NS) & 1, p.err); };
+      for (int k = 0; ok && part_segment<NT, KT>(p, k, seg); ++k) {
+        ok = mbar_wait(q_full, k & 1, p.err) && landed(seq);
+        if (!ok) break;
+        tc_fence_after();
+        for (int i = 0; i < NT; ++i) mma_s(i, seq % NS);
+        umma_commit(&empty[seq % NS]);
+        if (seg.n_tiles == 1) umma_commit(q_empty);
+        ++seq;
+        for (int t = 0; ok && t < seg.n_tiles; ++t) {
+          const bool more = t + 1 < seg.n_tiles;
+          const unsigned kq = seq, vq = more ? seq + 1 : seq;
+          for (int i = 0; ok && i < NT; ++i) {
+            ok = mbar_wait(&p_full[i], (tiles + t) & 1, p.err);
+            if (ok && i == 0) ok = landed(vq);
+            // the first P V of a segment overwrites O: the last one's must be read
+            if (ok && t == 0) ok = mbar_wait(&o_free[i], (k & 1) ^ 1u, p.err);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk)
+              part_mma_ts(col_o(i), col_s(i) + kk * 8,
+                          umma_desc_sw128_mn(smem_u32(ring(vq % NS) + kk * 16 * 128), KT * 128,
+                                             1024),
+                          id_o, (t > 0 || kk > 0) ? 1u : 0u);
+            if (!more) umma_commit(&o_full[i]);
+            if (more) {
+              if (i == 0) {
+                ok = landed(kq);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              mma_s(i, kq % NS);
+            }
+          }
+          if (!ok) break;
+          if (more) umma_commit(&empty[kq % NS]);
+          umma_commit(&empty[vq % NS]);
+          if (t + 2 == seg.n_tiles) umma_commit(q_empty);
+          seq = vq + 1;
+        }
+        tiles += seg.n_tiles;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int i = (warp - 2) >> 2;                   // row tile
+    const int sp = warp & 3;                         // tensor-memory sub-partition
+    const int r = 32 * sp + lane;                    // row of the tile
+    const uint32_t lanes = static_cast<uint32_t>(32 * sp) << 16;
+    const float scale = p.scale_log2;
+    unsigned tiles = 0, seq = 0;
+    bool ok = true;
+    for (int k = 0; part_segment<NT, KT>(p, k, seg); ++k) {
+      // keys that this row sees: none if it is no row of this segment
+      int limit = 0;
+      {
+        const int tr = r / p.G;
+        const int tok = seg.tok0 + i * p.tpt + tr;
+        if (tr < p.tpt && tok < p.n_tok) {
+          const int b = tok / p.q_len, j = tok - b * p.q_len;
+          const int n = p.seq_lens[b];
+          if ((seg.b < 0 || seg.b == b) && n >= 0)
+            limit = static_cast<int>(min(static_cast<long long>(n) + (p.causal ? j + 1 : p.q_len),
+                                         static_cast<long long>(seg.key1)));
+        }
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int t = 0; t < seg.n_tiles; ++t) {
+        if (ok) ok = mbar_wait(&s_full[i], (tiles + t) & 1, p.err);
+        tc_fence_after();
+        float x[KT];
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c) tmem_ld_32x32b_x32(col_s(i) + lanes + c * 32, x + c * 32);
+        tmem_ld_wait();
+        const int left = limit - (seg.key0 + t * KT);    // keys of the tile that the row sees
+        if (__any_sync(0xffffffffu, left < KT)) {
+#pragma unroll
+          for (int c = 0; c < KT; ++c)
+            if (c >= left) x[c] = -INFINITY;
+        }
+        float mx = x[0];
+#pragma unroll
+        for (int c = 1; c < KT; ++c) mx = fmaxf(mx, x[c]);
+        mx *= scale;
+        // The reference is the first maximum that the row meets; it is raised
+        // only when a score outgrows it by the headroom (2^32 keeps P, l and O
+        // far inside their types), so O is rarely rescaled.
+        if (__any_sync(0xffffffffu, mx > m + kPartHeadroom)) {
+          const float up = mx > m + kPartHeadroom ? mx : m;
+          const float a = m == -INFINITY ? 0.f : part_ex2(m - up);
+          const bool has = __any_sync(0xffffffffu, m != -INFINITY);
+          m = up;
+          l *= a;
+          if (has && t > 0) {     // P V of the tile before has run: s_full came after it
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld_32x32b_x32(col_o(i) + lanes + c * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= a;
+              uint32_t w[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e]);
+              part_st_x32(col_o(i) + lanes + c * 32, w);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int c = 0; c < KT / 64; ++c) {
+          uint32_t w[32];
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float a = part_ex2(fmaf(x[c * 64 + 2 * e], scale, -ref));
+            const float b = part_ex2(fmaf(x[c * 64 + 2 * e + 1], scale, -ref));
+            l0 += a;
+            l1 += b;
+            w[e] = pack_bf16x2(a, b);
+          }
+          l += l0 + l1;
+          part_st_x32(col_s(i) + lanes + c * 32, w);
+        }
+        if (NT == 1 && sp == 0 && t + 1 == seg.n_tiles && (seg.key1 & 15)) {
+          // rows of V past the last key of its page may hold anything (NaN too):
+          // zeros there, so that P = 0 adds 0
+          const unsigned vq = seq + 2 * seg.n_tiles - 1;
+          if (ok) ok = mbar_wait(&full[vq % NS], (vq / NS) & 1, p.err);
+          const int end = seg.key1 - (seg.key0 + t * KT);
+          const int n16 = (16 - (end & 15)) * kHalves * 8;
+          for (int e = lane; e < n16; e += 32) {
+            const int hf = e & (kHalves - 1), cc = (e / kHalves) & 7, rr = end + e / (kHalves * 8);
+            *reinterpret_cast<uint4*>(ring(vq % NS) + hf * KT * 128 + rr * 128 + cc * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          part_fence_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[i]);
+      }
+      // the part: O, and (m, l) of the row
+      if (ok) ok = mbar_wait(&o_full[i], k & 1, p.err);
+      tc_fence_after();
+      const bool own = seg.b >= 0;
+      float* dst = own ? p.own_o + (static_cast<size_t>(seg.slot) * p.R + r) * D
+                       : p.prefix_o + ((static_cast<size_t>(seg.slot) * NT + i) * 128 + r) * D;
+      const bool store = ok && l != 0.f &&   // a NaN is a result
+                          (!own || r < p.R);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        tmem_ld_32x32b_x32(col_o(i) + lanes + c * 32, o);
+        tmem_ld_wait();
+        if (store) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(dst + c * 32 + e) =
+                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free[i]);
+      if (own) {
+        if (r < p.R) p.own_ml[static_cast<size_t>(seg.slot) * p.R + r] = make_float2(m, l);
+      } else {
+        p.prefix_ml[(static_cast<size_t>(seg.slot) * NT + i) * 128 + r] = make_float2(m, l);
+      }
+      tiles += seg.n_tiles;
+      seq += 2 * seg.n_tiles;
+    }
+  }
+  tc_fence_before();
+  cta_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+// One warp joins the parts of one (token, query head); prefix_nt, prefix_kt: the
+// row tiles and keys a tile of the kernel that ran the prefix.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int prefix_nt,
+                                                        f16* __restrict__ out) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int kPer = D / 32;
+  const int unit = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (unit >= p.n_tok * p.Hq) return;
+  const int tok = unit / p.Hq, head = unit - tok * p.Hq;
+  const int h = head / p.G, g = head - h * p.G;
+  const int b = tok / p.q_len, j = tok - b * p.q_len;
+  const int seq = p.seq_lens[b];
+  if (seq < 0) return;                       // a padding request keeps its rows
+  float M = -INFINITY, l = 0.f, acc[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  auto add = [&](const float2 ml, const float* o) {
+    if (ml.y == 0.f) return;               // the row saw no key of this part
+    const float top = fmaxf(M, ml.x);
+    const float keep = M == -INFINITY ? 0.f : part_ex2(M - top), w = part_ex2(ml.x - top);
+    M = top;
+    l = l * keep + ml.y * w;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * keep + o[lane * kPer + e] * w;
+  };
+  if (p.prefix_ctas > 0) {
+    const int tile = tok / p.tpt, rg = tile / prefix_nt;
+    const int item = h * p.row_groups + rg;
+    const int row = (tok - tile * p.tpt) * p.G + g;
+    const long long units = static_cast<long long>(p.prefix_items) * p.prefix_tiles;
+    const long long a = static_cast<long long>(item) * p.prefix_tiles, e = a + p.prefix_tiles;
+    int c = static_cast<int>(a * p.prefix_ctas / units);
+    while (c + 1 < p.prefix_ctas && part_begin(units, p.prefix_ctas, c + 1) <= a) ++c;
+    while (c > 0 && part_begin(units, p.prefix_ctas, c) > a) --c;
+    for (; c < p.prefix_ctas && part_begin(units, p.prefix_ctas, c) < e; ++c) {
+      const long long u0 = part_begin(units, p.prefix_ctas, c);
+      if (part_begin(units, p.prefix_ctas, c + 1) <= max(a, u0)) continue;   // nothing dealt
+      const int k = item - static_cast<int>(u0 / p.prefix_tiles);
+      const size_t at = ((static_cast<size_t>(c) * p.max_segs + k) * prefix_nt +
+                         (tile - rg * prefix_nt)) * 128 + row;
+      add(p.prefix_ml[at], p.prefix_o + at * D);
+    }
+  }
+  const long long own = static_cast<long long>(seq) + p.q_len - p.prefix_keys;
+  if (own > static_cast<long long>(p.W) * 16 - p.prefix_keys && lane == 0 && j == 0 && head == 0)
+    raise_error(p.err, DFLASH_DEVERR_TABLE);
+  for (int s = 0; s < p.max_splits && static_cast<long long>(s) * p.chunk_keys < own; ++s) {
+    const size_t at = ((static_cast<size_t>(s) * p.B + b) * p.Hkv + h) * p.R + j * p.G + g;
+    add(p.own_ml[at], p.own_o + at * D);
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  f16* o = out + static_cast<size_t>(unit) * D + lane * kPer;
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2)
+    *reinterpret_cast<uint32_t*>(o + e) = pack_f16x2(acc[e] * inv, acc[e + 1] * inv);
+}
+
+}  // namespace dflash

@@ -170,6 +170,9 @@ def lib() -> ctypes.CDLL:
                               vp], i32),
         "dflash_block_attention": ([vp, vp, vp, vp, i32, i32, vp, vp, i32, vp, vp, sz, vp],
                                    i32),
+        "dflash_prefix_attention_workspace_bytes": ([vp, i32, i32, i32, i32], sz),
+        "dflash_prefix_attention": ([vp, vp, i32, i32, vp, vp, i32, i32, i32, vp, vp, i32, vp, vp,
+                                     sz, vp], i32),
         "dflash_plan_attention_info": ([i32] * 10 + [ctypes.POINTER(_AttnPlan)], i32),
         "dflash_check_device_errors": ([vp, ctypes.POINTER(ctypes.c_uint)], i32),
         "dflash_launch_count": ([vp], ctypes.c_ulonglong),
@@ -598,6 +601,46 @@ class DFlash:
                                             int(k_cache.shape[0]), _ptr(o), _ptr(ws),
                                             ws.numel(), _stream(stream)),
                "dflash_block_attention")
+        return o
+
+    def prefix_attention_workspace_bytes(self, B: int, q_len: int, max_pages_per_seq: int,
+                                         prefix_pages: int) -> int:
+        return lib().dflash_prefix_attention_workspace_bytes(self.h, B, q_len, max_pages_per_seq,
+                                                             prefix_pages)
+
+    def prefix_attention(self, q, seq_lens, block_table, prefix_pages: int, k_cache, v_cache,
+                         causal: bool = False, o=None, workspace=None, stream=None):
+        """Attention of q [B*q_len, Hq, d] over a batch whose first
+        ``prefix_pages`` pages (block_table's row 0) are the same for every
+        request (dflash_prefix_attention).  Returns o [B*q_len, Hq*d] fp16."""
+        B, W, c = int(seq_lens.shape[0]), int(block_table.shape[1]), self.cfg
+        hkv, hq, d = c["n_kv_heads"] // self.tp[1], c["n_q_heads"] // self.tp[1], c["head_dim"]
+        n = int(q.shape[0])
+        _want(q, torch.bfloat16, "q")
+        _want(seq_lens, torch.int32, "seq_lens")
+        _want(block_table, torch.int32, "block_table")
+        if tuple(q.shape[1:]) != (hq, d) or (n % B if B else n):
+            raise ValueError(f"q: expected [{B} * q_len, {hq}, {d}]")
+        if int(block_table.shape[0]) != B:
+            raise ValueError(f"block_table: expected {B} rows")
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            _want(t, torch.bfloat16, name)
+            if tuple(t.shape) != (k_cache.shape[0], hkv, c.get("page_size", 16), d):
+                raise ValueError(f"{name}: expected [num_pages, {hkv}, page_size, {d}]")
+        if o is None:
+            o = torch.empty(n, hq * d, dtype=torch.float16, device=self.device)
+        _want(o, torch.float16, "o")
+        if o.numel() != n * hq * d:
+            raise ValueError(f"o: expected [{n}, {hq * d}]")
+        q_len = n // B if B else 1
+        ws = workspace
+        if ws is None:
+            ws = self.ws.get(self.prefix_attention_workspace_bytes(B, q_len, W, prefix_pages))
+        _check(lib().dflash_prefix_attention(self.h, _ptr(q), q_len, int(causal), _ptr(seq_lens),
+                                             _ptr(block_table), B, W, prefix_pages, _ptr(k_cache),
+                                             _ptr(v_cache), int(k_cache.shape[0]), _ptr(o),
+                                             _ptr(ws), ws.numel(), _stream(stream)),
+               "dflash_prefix_attention")
         return o
 
     # ---------------------------------------------------------- diagnostics

@@ -651,6 +651,36 @@ dflash_status dflash_block_attention(dflash_handle* h, const void* q, const int3
                                      void* o, void* workspace, size_t workspace_bytes,
                                      void* stream);
 
+/* The attention of dflash_block_attention for a batch whose requests share their
+ * first pages (one system prompt, one document): the shared keys are read once
+ * for all rows instead of once per request.  Also for other query lengths than
+ * the handle's block_size, down to single tokens, and causal inside the block.
+ *   q [B*q_len, n_q_heads, head_dim] bf16 (q_len rows per request, request order)
+ *   o [B*q_len, n_q_heads*head_dim] fp16 out
+ *   prefix_pages: the first prefix_pages entries of block_table's row 0 hold
+ *     keys [0, prefix_pages * page_size) of EVERY request (the entries of the
+ *     other rows there are not read); 0: nothing is shared
+ * Row i of request b attends to keys [0, seq_lens[b] + q_len), with causal != 0
+ * to [0, seq_lens[b] + i + 1); seq_lens[b] may end inside the prefix.  A negative
+ * seq_lens[b] marks a padding request: its rows of o stay as they were.
+ * Scores and sums in fp32; a weight is rounded to bf16 once (2^-8 relative to
+ * itself) before it multiplies V.  A value of V that is not finite reaches every
+ * row of its request's block, masked or not; other masked or unused places of
+ * the pools may hold anything.  Pages outside the pool or past the table
+ * (DFLASH_DEVERR_SLOT, DFLASH_DEVERR_TABLE) are not read.
+ * q_len * (n_q_heads / n_kv_heads) > 128, B > 65535, max_pages_per_seq > 2^24 or
+ * num_pages * n_kv_heads * page_size > 2^31 - 1 is DFLASH_ERR_UNSUPPORTED_SHAPE;
+ * q, o and the pools are 16-byte aligned, the workspace 256-byte aligned.
+ * B == 0 is a no-op.  Needs dflash_prefix_attention_workspace_bytes. */
+size_t dflash_prefix_attention_workspace_bytes(const dflash_handle* h, int B, int q_len,
+                                               int max_pages_per_seq, int prefix_pages);
+dflash_status dflash_prefix_attention(dflash_handle* h, const void* q, int q_len, int causal,
+                                      const int32_t* seq_lens, const int32_t* block_table, int B,
+                                      int max_pages_per_seq, int prefix_pages,
+                                      const void* k_cache, const void* v_cache, int num_pages,
+                                      void* o, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
 /* The attention launch plan that a proposal with this geometry uses
  * (diagnostics; host only, no device needed): kv groups of bs * G query rows
  * (G = query heads per kv head), block tables of W pages of P keys, on

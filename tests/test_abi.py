@@ -145,3 +145,5 @@ def test_operator_calls_validate_on_the_host(L):
     assert f(one, one, 10, 2, 3, 10, z, z, z, z, one, one, one, one, one, z, one, 8, z) == -3
     assert L.dflash_verify_sampled_workspace_bytes(2, 3) >= 2 * 6 * 4
     assert L.dflash_verify_sampled_workspace_bytes(0, 3) == 0
+    assert L.dflash_prefix_attention(z, z, 1, 0, z, z, 0, 4, 0, z, z, 1, z, z, 0, z) == -1
+    assert L.dflash_prefix_attention_workspace_bytes(z, 1, 1, 4, 0) == 0
