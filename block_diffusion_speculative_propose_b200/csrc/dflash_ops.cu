@@ -47,13 +47,11 @@ void launch_append(dflash_handle* h, const AppendParams& p, cudaStream_t st) {
 // at most eight CTAs (the portable cluster size).
 struct SamplePlan {
   int ranks = 1, slice = 0;
-  size_t smem = 0;
 };
 SamplePlan plan_sample(int V) {
   SamplePlan p;
   while (p.ranks < kSmpMaxCluster && p.ranks * 8192 < V) p.ranks *= 2;
   p.slice = (cdiv(V, p.ranks) + 3) / 4 * 4;
-  p.smem = smp_smem_bytes(p.slice);
   return p;
 }
 
@@ -310,10 +308,8 @@ dflash_status dflash_sample_tokens(const float* logits, int64_t ld, int rows, in
   p.tokens = tokens;
   p.probs = probs;
   p.err = device_error;
-  DF_CUDA(cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(pl.smem)));
   launch_kc(pdl_default(), pl.ranks, sample_kernel, dim3(pl.ranks, rows), dim3(kSmpThreads),
-            pl.smem, st, p);
+            0, st, p);
   return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 
@@ -359,12 +355,13 @@ dflash_status dflash_verify_sampled(const int32_t* drafts, const float* target_l
   p.done = static_cast<unsigned*>(workspace);
   p.refused = p.done + B;
   p.row_token = static_cast<int32_t*>(workspace) + 2 * static_cast<int64_t>(B);
-  DF_CUDA(cudaFuncSetAttribute(verify_sampled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(pl.smem)));
   launch_k(pdl_default(), zero_words_kernel, dim3(std::min(cdiv(2 * B, 256), 64)), dim3(256), 0,
            st, p.done, 2 * B);
-  launch_kc(pdl_default(), pl.ranks, verify_sampled_kernel, dim3(pl.ranks, B, K + 1),
-            dim3(kSmpThreads), pl.smem, st, p);
+  // Few rows all run at once; of many, a cluster takes a run of a request's rows,
+  // so that the ones behind a refused draft cost no launch.
+  p.run = std::max(1, std::min(8, B * (K + 1) / 96));
+  launch_kc(pdl_default(), pl.ranks, verify_sampled_kernel, dim3(pl.ranks, B, cdiv(K + 1, p.run)),
+            dim3(kSmpThreads), 0, st, p);
   return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 

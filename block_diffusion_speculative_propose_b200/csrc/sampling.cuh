@@ -14,25 +14,38 @@
 // order (V <= 2^18.6 weights of at most 2^44).  Tokens below 2^-45 of the
 // largest weigh nothing.
 //
-// Layout.  A row is held by a cluster: each of its CTAs copies one slice of the
-// row to shared memory, so the logits are read from memory once however many
-// passes the filters need; what the CTAs have to tell one another goes through
-// distributed shared memory.
+// Layout.  A cluster takes a row, each of its CTAs a slice.  The first pass
+// brings the row from memory and finds the maxima; whatever the filters then
+// need is read again while it still lies in L2, so a CTA holds no tokens and four
+// of them share an SM, which hides what a row waits for (three cluster barriers
+// and the tail in which one CTA sorts).  What the CTAs have to tell one another
+// is pushed into each other's shared memory before a barrier.
+//
+// Work.  Only a row without top_k needs the weight of every token (the sums that
+// u and top_p refer to); it costs about nine 64-bit operations.  A top_k needs
+// no second pass: the k-th largest of the threads' own maxima bounds the k-th
+// largest token from below, and only threads whose maximum reaches that bound
+// look at their tokens again.  The candidates, a few more than k, are sorted.
 #pragma once
 
 #include "dflash_device.cuh"
 
 namespace dflash {
 
-constexpr int kSmpThreads = 512;
+constexpr int kSmpThreads = 256;
 constexpr int kSmpWarps = kSmpThreads / 32;
+constexpr int kSmpCtas = 4;           // of an SM
 constexpr int kSmpMaxCluster = 8;
 constexpr int kSmpBins = 1024;        // linear bins of x below the maximum
 constexpr int kSmpRadix = 2048;       // bins of a radix level (11 bits)
 constexpr int kSmpList = 1024;        // candidates that one CTA sorts
+constexpr int kSmpFew = 128;          // candidates that are ranked by comparing all pairs
+constexpr int kSmpListTopK = 640;     // largest top_k whose candidates are gathered by maxima
+constexpr int kSmpAim = 512;          // candidates gathered for a top_p alone
 constexpr int kSmpOneBits = 44;       // W of the largest weight: 2^44
 constexpr float kSmpReach = 31.9f;    // 46 ln 2: tokens further below weigh nothing
-constexpr int kSmpMaxVocab = 393216;  // 8 slices of 192 KiB
+constexpr int kSmpTab = 512;          // 2^(j / 512)
+constexpr int kSmpMaxVocab = 393216;  // V 2^44 < 2^63
 
 typedef unsigned long long u64;
 
@@ -43,40 +56,52 @@ struct SampleSettings {
   const float* min_p;         // null: 0
 };
 
-// What the CTAs of a cluster show one another; every field is written once a
-// row, so a barrier between the writing and the reading is all it needs.
+// Every field that a peer writes or reads is used once a row, so a barrier
+// between the writing and the reading is all it needs.
 struct SmpShared {
-  double tab[32];                    // 2^(j / 32)
+  double tab[kSmpTab];
   u64 warp_a[kSmpWarps];             // block-wide sums
   u64 bcast[4];
-  u64 top_key;                       // phase A: largest (value, id)
-  float low;                         // phase A: smallest finite value
-  u64 mass_all;                      // weight of the whole slice
-  u64 ties[2];                       // ties of the border value (two searches)
+  u64 mass_in[kSmpMaxCluster];       // from each rank: the weight of its slice
+  u64 kept_in[kSmpMaxCluster];       // from each rank: its kept weight, the draft's
+  u64 draft_in[kSmpMaxCluster];
+  u64 ties_in[2][kSmpMaxCluster];    // from each rank: ties of the border value (two searches)
   u64 border[2];                     // the border key (two searches)
-  u64 kept, draft_w;                 // the slice's kept weight, the draft's weight
-  unsigned n_local;
+  u64 told, n_keep;                  // from rank 0: how a search goes on
+  float top_in[kSmpMaxCluster];      // from each rank: the largest value of its slice
+  float thr_in[kSmpMaxCluster][4];   // and values that ever fewer of its tokens reach
+  float thr[4];
+  unsigned first_in[kSmpMaxCluster]; // greedy: the first id that holds the largest value
+  unsigned first;
+  unsigned n_list[3];                // rank 0: candidates gathered (three lists)
+  unsigned n_own, own_at;            // this CTA's share of them, its place
+  unsigned verdict, told32;          // from rank 0
   unsigned first_bad;
-  unsigned cnt[kSmpRadix];           // histogram: tokens
   union {
-    unsigned mass[2][kSmpRadix];     // histogram: low and high words of weights
+    __align__(16) unsigned cnt[kSmpRadix];   // histogram: tokens
+    u64 own[kSmpList];                       // this CTA's candidates
+  };
+  union {
+    __align__(16) unsigned mass[2][kSmpRadix];   // histogram: low, high words of weights
     struct {
-      u64 list[kSmpList];            // rank 0: the candidates' keys
+      u64 list[kSmpList];                        // rank 0: the candidates' keys
       u64 w[kSmpList];
     };
   };
 };
 
-__host__ __device__ constexpr size_t smp_smem_bytes(int slice) {
-  return sizeof(SmpShared) + static_cast<size_t>(slice) * 4 + 16;
+__device__ __forceinline__ float smp_norm(float x) {       // NaN as -inf, -0 as +0
+  return fmaxf(x, -INFINITY) + 0.f;
 }
-
 __device__ __forceinline__ uint32_t smp_order(float x) {   // orders like x (no NaN, no -0)
   const uint32_t b = __float_as_uint(x);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 __device__ __forceinline__ float smp_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+__device__ __forceinline__ float smp_key_value(u64 key) {
+  return smp_value(static_cast<uint32_t>(key >> 32));
 }
 __device__ __forceinline__ u64 smp_key(float x, uint32_t id) {
   return (static_cast<u64>(smp_order(x)) << 32) | (0xffffffffu - id);
@@ -85,22 +110,18 @@ __device__ __forceinline__ uint32_t smp_id(u64 key) {
   return 0xffffffffu - static_cast<uint32_t>(key);
 }
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
+}
+__device__ __forceinline__ uint4 ld_peer_v4(const void* p, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(peer_addr(p, rank))
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ u64 ld_peer_u64(const void* p, uint32_t rank) {
   u64 v;
@@ -114,6 +135,17 @@ __device__ __forceinline__ uint32_t ld_peer_u32(const void* p, uint32_t rank) {
 }
 __device__ __forceinline__ void st_peer_u64(void* p, uint32_t rank, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer_addr(p, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_peer_u32(void* p, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_addr(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t add_peer_u32(void* p, uint32_t rank, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
+               : "=r"(old)
+               : "r"(peer_addr(p, rank)), "r"(v)
+               : "memory");
+  return old;
 }
 
 __device__ __forceinline__ u64 warp_sum_u64(u64 v) {
@@ -133,37 +165,65 @@ __device__ __forceinline__ u64 warp_scan_u64(u64 v, int lane) {   // inclusive
 // One row as the cluster's threads see it.
 struct SmpRow {
   SmpShared* sh;
-  const float* x;        // this CTA's slice (NaN as -inf, -0 as +0)
-  int len, begin;        // its length and first id
+  const float* x;        // this CTA's slice
+  int len, padded, begin;   // its length, that rounded up to whole warp loads, its first id
+  bool wide;             // its 16-byte loads are aligned
   int rank, ranks;
   float m;               // the row's largest value
-  double c;              // log2(e) / T
+  float x_cut;           // weighs nothing
+  double md, c;          // m, 512 log2(e) / T
   u64 w_min;             // min_p as a weight
+  bool fast;             // x_cut is between 46 and 60 bits below m
 };
 
-// W of value x: 0 where it is filtered by min_p or weighs nothing.  With
-// t = (x - m) log2(e) / T = n/32 + f, 2^t = 2^(n >> 5) 2^((n & 31) / 32) 2^f,
-// |f| <= 1/64: five terms of 2^f's Taylor series leave 2^-48 relative.
-__device__ __forceinline__ u64 smp_weight(const SmpRow& r, float x) {
-  const double d = x == r.m ? 0.0 : static_cast<double>(x) - static_cast<double>(r.m);
-  const double t = d * r.c;
-  if (!(t >= -46.0)) return 0ull;
-  const double magic = 6755399441055744.0;   // 1.5 2^52: the sum's low bits are rint(32 t)
-  const double s = __fma_rn(t, 32.0, magic);
+// Tokens i .. i+3 of the slice, -inf past its end (i a multiple of four).
+__device__ __forceinline__ float4 smp_load4(const SmpRow& r, int i) {
+  if (r.wide && i + 4 <= r.len) return __ldg(reinterpret_cast<const float4*>(r.x + i));
+  float4 v;
+  v.x = i < r.len ? __ldg(r.x + i) : -INFINITY;
+  v.y = i + 1 < r.len ? __ldg(r.x + i + 1) : -INFINITY;
+  v.z = i + 2 < r.len ? __ldg(r.x + i + 2) : -INFINITY;
+  v.w = i + 3 < r.len ? __ldg(r.x + i + 3) : -INFINITY;
+  return v;
+}
+
+// An integer W plus kSmpBias, the bits of 2^52: sums of these wrap, and the
+// bias is taken out of a sum at its end.
+constexpr u64 kSmpBias = 0x4330000000000000ull;
+
+// W + bias of value x: with t = (x - m) log2(e) / T = n/512 + f / 512,
+// 2^t = 2^(n >> 9) 2^((n & 511) / 512) 2^(f / 512), |f| <= 1/2: three terms of
+// the last factor's Taylor series leave (ln 2 / 1024)^4 / 24 < 2^-46.
+__device__ __forceinline__ u64 smp_bits(const SmpRow& r, float x) {
+  const double d = static_cast<double>(fmaxf(x, r.x_cut)) - r.md;   // a NaN is cut too
+  const double magic = 6755399441055744.0;   // 1.5 2^52: the sum's low bits are the integer
+  const double s = __fma_rn(d, r.c, magic);
   const int n = __double2loint(s);
-  const double f = __fma_rn(t, 32.0, magic - s);
-  const double a = 0.6931471805599453 / 32.0;   // ln 2 / 32
-  double p = a * a * a * a * a / 120.0;
-  p = __fma_rn(p, f, a * a * a * a / 24.0);
-  p = __fma_rn(p, f, a * a * a / 6.0);
-  p = __fma_rn(p, f, a * a / 2.0);
+  const double f = __fma_rn(d, r.c, magic - s);
+  constexpr double a = 0.6931471805599453 / kSmpTab;   // ln 2 / 512
+  double p = __fma_rn(f, a * a * a / 6.0, a * a / 2.0);
   p = __fma_rn(p, f, a);
   p = __fma_rn(p, f, 1.0);
-  p *= r.sh->tab[n & 31];
-  // times 2^((n >> 5) + 44), then the integer nearest (n >> 5 >= -46: normal)
-  const double v = __hiloint2double(__double2hiint(p) + (((n >> 5) + kSmpOneBits) << 20),
+  p *= r.sh->tab[n & (kSmpTab - 1)];
+  // times 2^((n >> 9) + 44) (a normal number: n >> 9 >= -61), then the integer nearest
+  const double v = __hiloint2double(__double2hiint(p) + (((n >> 9) + kSmpOneBits) << 20),
                                     __double2loint(p));
-  const u64 w = static_cast<u64>(__double_as_longlong(v + 4503599627370496.0)) & 0xfffffffffffffull;
+  return static_cast<u64>(__double_as_longlong(v + 4503599627370496.0));
+}
+
+// W of value x: 0 where it is filtered by min_p or weighs nothing.
+__device__ __forceinline__ u64 smp_weight(const SmpRow& r, float x) {
+  u64 w;
+  if (r.fast) {
+    w = smp_bits(r, x) - kSmpBias;
+  } else if (x == r.m) {
+    w = 1ull << kSmpOneBits;
+  } else {
+    // a temperature so small, or so large, or values so large that no cut in
+    // fp32 serves: the same by the library's exponential
+    const double t = (static_cast<double>(x) - r.md) * r.c / kSmpTab + kSmpOneBits;
+    w = t >= -2.0 ? static_cast<u64>(__double2ll_rn(exp2(t))) : 0ull;   // NaN: 0
+  }
   return w < r.w_min ? 0ull : w;
 }
 
@@ -174,7 +234,10 @@ __device__ __forceinline__ u64 smp_block_sum(SmpShared* sh, u64 v) {
   __syncthreads();
   if (lane == 0) sh->warp_a[warp] = v;
   __syncthreads();
-  return warp_sum_u64(lane < kSmpWarps ? sh->warp_a[lane] : 0ull);
+  v = 0;
+#pragma unroll
+  for (int w = 0; w < kSmpWarps; ++w) v += sh->warp_a[w];
+  return v;
 }
 // Block-wide inclusive scan of one value a thread (in thread order).
 __device__ __forceinline__ u64 smp_block_scan(SmpShared* sh, u64 v) {
@@ -183,16 +246,22 @@ __device__ __forceinline__ u64 smp_block_scan(SmpShared* sh, u64 v) {
   __syncthreads();
   if (lane == 31) sh->warp_a[warp] = v;
   __syncthreads();
-  const u64 before = warp_sum_u64(lane < warp ? sh->warp_a[lane] : 0ull);
-  return v + before;
+#pragma unroll
+  for (int w = 0; w < kSmpWarps; ++w)
+    if (w < warp) v += sh->warp_a[w];
+  return v;
 }
 
-// Falling bitonic sort of a[0..n), n a power of two.
-__device__ __forceinline__ void smp_sort(u64* a, int n) {
-  for (int k = 2; k <= n; k <<= 1)
+// Falling bitonic sort of a[0..n), n <= kSmpList.
+__device__ __noinline__ void smp_sort(u64* a, int n) {
+  const int tid = threadIdx.x;
+  int n2 = 64;
+  while (n2 < n) n2 <<= 1;
+  for (int i = n + tid; i < n2; i += kSmpThreads) a[i] = 0;
+  for (int k = 2; k <= n2; k <<= 1)
     for (int j = k >> 1; j > 0; j >>= 1) {
       __syncthreads();
-      for (int i = threadIdx.x; i < n / 2; i += kSmpThreads) {
+      for (int i = tid; i < n2 / 2; i += kSmpThreads) {
         const int lo = 2 * i - (i & (j - 1));
         const u64 p = a[lo], q = a[lo + j];
         if ((p < q) == ((lo & k) == 0)) {
@@ -204,112 +273,195 @@ __device__ __forceinline__ void smp_sort(u64* a, int n) {
   __syncthreads();
 }
 
-// The border of a kept prefix among the tokens with key >= floor_key: the key
-// of the `want`-th of them (by_mass false), or of the first at which their
-// running weight reaches top_p of all of theirs.  Every CTA of the cluster
-// takes part and gets the same answer.  Three radix levels find the value, then
-// the ties at it are counted in vocabulary order; `which` (0, 1) separates the
-// shared fields of a row's two searches.
-__device__ u64 smp_border(const SmpRow& r, bool by_mass, u64 floor_key, u64 want, double top_p,
-                          int which) {
-  SmpShared* sh = r.sh;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint32_t prefix = 0;
-  u64 base = 0;             // tokens, or weight, above the current prefix
-  double goal = 0.0;        // by mass: the weight to reach
-  u64 bin_cnt = 0;
-  constexpr int kPer = kSmpRadix / kSmpThreads;
-  for (int level = 0; level < 3; ++level) {
-    const int bits = level == 2 ? 10 : 11;
-    const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
-    for (int i = tid; i < kSmpRadix; i += kSmpThreads) {
-      sh->cnt[i] = 0;
+// The linear bin of x below the maximum: fp32 2^23 + (m - x) scale rounds to an
+// integer, and its bits order like it (a NaN comes last).
+__device__ __forceinline__ unsigned smp_bin(float m, float scale, float x) {
+  return __float_as_uint(fmaf(m - x, scale, 8388608.f)) - 0x4B000000u;
+}
+
+// One candidate into this CTA's own list / that list into rank 0's, counted in
+// n_list[which] (past its room nothing is stored, only counted).
+__device__ __forceinline__ void smp_candidate(SmpShared* sh, float x, int id) {
+  const unsigned at = atomicAdd(&sh->n_own, 1u);
+  if (at < kSmpList) sh->own[at] = smp_key(smp_norm(x), id);
+}
+__device__ __forceinline__ void smp_hand_over(SmpShared* sh, int which) {
+  __syncthreads();
+  const unsigned n = sh->n_own;
+  if (threadIdx.x == 0 && n) sh->own_at = add_peer_u32(&sh->n_list[which], 0, n);
+  __syncthreads();
+  const unsigned at = sh->own_at;
+  for (unsigned i = threadIdx.x; i < min(n, static_cast<unsigned>(kSmpList)) && at + i < kSmpList;
+       i += kSmpThreads)
+    st_peer_u64(&sh->list[at + i], 0, sh->own[i]);
+}
+
+__device__ __forceinline__ void smp_clear(SmpShared* sh, int bins, bool by_mass) {
+  for (int i = threadIdx.x; i < bins; i += kSmpThreads) {
+    sh->cnt[i] = 0;
+    if (by_mass) {
       sh->mass[0][i] = 0;
       sh->mass[1][i] = 0;
     }
-    __syncthreads();
-    for (int i = tid; i < r.len; i += kSmpThreads) {
-      const float x = r.x[i];
-      const u64 key = smp_key(x, r.begin + i);
-      const uint32_t o = static_cast<uint32_t>(key >> 32);
-      if (key < floor_key || (level > 0 && (o >> (shift + bits)) != prefix)) continue;
-      const uint32_t b = (o >> shift) & ((1u << bits) - 1);
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ void smp_count(SmpShared* sh, unsigned b, bool by_mass, u64 w) {
+  if (by_mass) {
+    const unsigned lo = static_cast<unsigned>(w);
+    const unsigned old = atomicAdd(&sh->mass[0][b], lo);
+    const unsigned hi = static_cast<unsigned>(w >> 32) + (old + lo < old ? 1u : 0u);
+    if (hi) atomicAdd(&sh->mass[1][b], hi);
+  }
+  atomicAdd(&sh->cnt[b], 1u);
+}
+
+struct SmpHit {
+  unsigned bin;      // in the histogram
+  u64 base, cnt;     // the measure before it, its tokens
+  u64 all;           // the measure of all bins
+};
+// Rank 0: the last bin that holds anything and starts before the goal - the one in
+// which it is reached, or, if rounding lets none reach it, the last of all.
+// Bins are taken in rising order, or (falling) from the last one down.  With
+// top_p >= 0 the goal becomes top_p of all.
+template <int BINS>
+__device__ SmpHit smp_merge(const SmpRow& r, bool by_mass, bool falling, u64 base, double top_p,
+                            double& goal) {
+  SmpShared* sh = r.sh;
+  const int tid = threadIdx.x;
+  constexpr int kPer = BINS / kSmpThreads;   // bins of a thread, a multiple of four
+  u64 v[kPer];
+  unsigned c[kPer];
+#pragma unroll
+  for (int q = 0; q < kPer; q += 4) {
+    const int b = (falling ? BINS - kPer - tid * kPer : tid * kPer) + q;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[q + e] = 0;
+      c[q + e] = 0;
+    }
+    for (int k = 0; k < r.ranks; ++k) {
+      const uint4 n = ld_peer_v4(&sh->cnt[b], k);
+      c[q] += n.x;
+      c[q + 1] += n.y;
+      c[q + 2] += n.z;
+      c[q + 3] += n.w;
       if (by_mass) {
-        const u64 w = smp_weight(r, x);
-        if (w == 0) continue;
-        const unsigned lo = static_cast<unsigned>(w);
-        const unsigned old = atomicAdd(&sh->mass[0][b], lo);
-        const unsigned hi = static_cast<unsigned>(w >> 32) + (old + lo < old ? 1u : 0u);
-        if (hi) atomicAdd(&sh->mass[1][b], hi);
+        const uint4 lo = ld_peer_v4(&sh->mass[0][b], k), hi = ld_peer_v4(&sh->mass[1][b], k);
+        v[q] += (static_cast<u64>(hi.x) << 32) + lo.x;
+        v[q + 1] += (static_cast<u64>(hi.y) << 32) + lo.y;
+        v[q + 2] += (static_cast<u64>(hi.z) << 32) + lo.z;
+        v[q + 3] += (static_cast<u64>(hi.w) << 32) + lo.w;
       }
-      atomicAdd(&sh->cnt[b], 1u);
+    }
+  }
+  u64 sum = 0;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    if (!by_mass) v[q] = c[q];
+    sum += v[q];
+  }
+  u64 run = smp_block_scan(sh, sum);
+  if (tid == kSmpThreads - 1) sh->bcast[0] = run;
+  if (tid == 0) sh->bcast[1] = 0;
+  __syncthreads();
+  SmpHit h;
+  h.all = sh->bcast[0];
+  if (top_p >= 0.0) goal = fmax(top_p * static_cast<double>(h.all), 1.0);   // the first is kept
+  run += base - sum;
+  int hit = -1;
+  u64 hit_base = 0, hit_cnt = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int q = falling ? kPer - 1 - j : j;
+    if (c[q] && static_cast<double>(run) < goal) {
+      hit = (falling ? BINS - kPer - tid * kPer : tid * kPer) + q;
+      hit_base = run;
+      hit_cnt = c[q];
+    }
+    run += v[q];
+  }
+  if (hit >= 0)
+    atomicMax(&sh->bcast[1], (static_cast<u64>(tid + 1) << 32) | static_cast<u64>(hit));
+  __syncthreads();
+  const u64 best = sh->bcast[1];
+  if (static_cast<int>(best >> 32) == tid + 1) {
+    sh->bcast[2] = hit_base;
+    sh->bcast[3] = hit_cnt;
+  }
+  __syncthreads();
+  h.bin = static_cast<unsigned>(best);
+  h.base = sh->bcast[2];
+  h.cnt = sh->bcast[3];
+  return h;
+}
+// Rank 0 tells every CTA; read as sh->told behind the next cluster barrier.
+__device__ __forceinline__ void smp_tell(const SmpRow& r, u64 v) {
+  if (threadIdx.x < r.ranks) st_peer_u64(&r.sh->told, threadIdx.x, v);
+}
+
+// The border of a kept prefix among the tokens with key >= floor_key: the key
+// of the `want`-th of them (by_mass false), or of the first at which their
+// running weight reaches top_p of all of theirs.  Every CTA of the cluster
+// takes part and gets the same answer.  `which` (0, 1) separates the shared
+// fields of a row's two searches.
+//
+// Three radix levels find the value, then the ties at it are counted in
+// vocabulary order: right for any values, slow where many share a bin.
+__device__ __noinline__ u64 smp_border_radix(const SmpRow& r, bool by_mass, u64 floor_key,
+                                             u64 want, double top_p, int which) {
+  SmpShared* sh = r.sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t prefix = 0;
+  u64 base = 0;             // rank 0: tokens, or weight, above the current prefix
+  u64 ties = 0;             // rank 0: tokens of the final value
+  double goal = static_cast<double>(want);
+  for (int level = 0; level < 3; ++level) {
+    const int bits = level == 2 ? 10 : 11;
+    const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
+    smp_clear(sh, kSmpRadix, by_mass);
+    for (int i0 = tid * 4; i0 < r.padded; i0 += kSmpThreads * 4) {
+      const float4 x4 = smp_load4(r, i0);
+      const float xs[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float x = smp_norm(xs[q]);
+        const u64 key = smp_key(x, r.begin + i0 + q);
+        const uint32_t o = static_cast<uint32_t>(key >> 32);
+        if (i0 + q >= r.len || key < floor_key || (level > 0 && (o >> (shift + bits)) != prefix))
+          continue;
+        u64 w = 0;
+        if (by_mass && (w = smp_weight(r, x)) == 0) continue;
+        smp_count(sh, (o >> shift) & ((1u << bits) - 1), by_mass, w);
+      }
     }
     cluster_sync();
-    // thread t holds bins from the top: index i = t * kPer + q is bin last - i
-    u64 c[kPer], v[kPer], sum = 0;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      const int b = kSmpRadix - 1 - (tid * kPer + q);
-      c[q] = v[q] = 0;
-      for (int k = 0; k < r.ranks; ++k) {
-        c[q] += ld_peer_u32(&sh->cnt[b], k);
-        if (by_mass)
-          v[q] += ld_peer_u32(&sh->mass[0][b], k) +
-                  (static_cast<u64>(ld_peer_u32(&sh->mass[1][b], k)) << 32);
-      }
-      if (!by_mass) v[q] = c[q];
-      sum += v[q];
+    if (r.rank == 0) {
+      const SmpHit h = smp_merge<kSmpRadix>(r, by_mass, true, base,
+                                            by_mass && level == 0 ? top_p : -1.0, goal);
+      base = h.base;
+      ties = h.cnt;
+      smp_tell(r, h.bin);
     }
-    u64 run = smp_block_scan(sh, sum);
-    if (level == 0 && by_mass) {
-      if (tid == kSmpThreads - 1) sh->bcast[0] = run;
-      __syncthreads();
-      goal = fmax(top_p * static_cast<double>(sh->bcast[0]), 1.0);   // the first is kept
-    }
-    run = base + run - sum;
-    // the last bin that holds tokens and starts before the goal: the one in
-    // which it is reached (or, if rounding lets none reach it, the last of all)
-    if (tid == 0) sh->bcast[1] = 0;
-    __syncthreads();
-    int hit = -1;
-    u64 hit_base = 0, hit_cnt = 0;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      if (c[q] && (by_mass ? static_cast<double>(run) < goal : run < want)) {
-        hit = kSmpRadix - 1 - (tid * kPer + q);
-        hit_base = run;
-        hit_cnt = c[q];
-      }
-      run += v[q];
-    }
-    if (hit >= 0)
-      atomicMax(&sh->bcast[1], (static_cast<u64>(tid + 1) << 32) | static_cast<u64>(hit));
-    __syncthreads();
-    const u64 best = sh->bcast[1];
-    if (static_cast<int>(best >> 32) == tid + 1) {
-      sh->bcast[2] = hit_base;
-      sh->bcast[3] = hit_cnt;
-    }
-    __syncthreads();
-    prefix = (prefix << bits) | static_cast<uint32_t>(best);
-    base = sh->bcast[2];
-    bin_cnt = sh->bcast[3];
-    cluster_sync();          // the histograms are cleared next
+    cluster_sync();
+    prefix = (prefix << bits) | static_cast<uint32_t>(sh->told);
   }
-  // all bin_cnt tokens here have the same value: how many of them are kept
-  const float tau = smp_value(prefix);
-  u64 n_keep;
-  if (by_mass) {
-    const u64 w = smp_weight(r, tau);
-    const double over = (goal - static_cast<double>(base)) / static_cast<double>(w);
-    n_keep = over >= static_cast<double>(bin_cnt) ? bin_cnt : static_cast<u64>(over);
-    while (n_keep < bin_cnt && static_cast<double>(base + n_keep * w) < goal) ++n_keep;
-    while (n_keep > 1 && static_cast<double>(base + (n_keep - 1) * w) >= goal) --n_keep;
-  } else {
-    n_keep = want - base;
+  // all tokens of this value weigh the same: how many of them are kept
+  if (r.rank == 0) {
+    u64 n_keep;
+    if (by_mass) {
+      const u64 w = smp_weight(r, smp_value(prefix));
+      const double over = (goal - static_cast<double>(base)) / static_cast<double>(w);
+      n_keep = over >= static_cast<double>(ties) ? ties : static_cast<u64>(over);
+      while (n_keep < ties && static_cast<double>(base + n_keep * w) < goal) ++n_keep;
+      while (n_keep > 1 && static_cast<double>(base + (n_keep - 1) * w) >= goal) --n_keep;
+    } else {
+      n_keep = want - base;
+    }
+    n_keep = max(1ull, min(ties, n_keep));
+    if (tid < r.ranks) st_peer_u64(&sh->n_keep, tid, n_keep);
   }
-  if (n_keep < 1) n_keep = 1;
-  if (n_keep > bin_cnt) n_keep = bin_cnt;
   // the n_keep-th tie in vocabulary order: warps own runs of the slice
   const int seg = ((r.len + kSmpWarps - 1) / kSmpWarps + 31) / 32 * 32;
   const int beg = min(r.len, warp * seg), end = min(r.len, beg + seg);
@@ -317,33 +469,129 @@ __device__ u64 smp_border(const SmpRow& r, bool by_mass, u64 floor_key, u64 want
   const u64 tie_hi = (static_cast<u64>(prefix) << 32) | 0xffffffffull;
   u64 mine = 0;
   for (int i = beg + lane; i < end; i += 32) {
-    const u64 key = smp_key(r.x[i], r.begin + i);
+    const u64 key = smp_key(smp_norm(__ldg(r.x + i)), r.begin + i);
     mine += key >= tie_lo && key <= tie_hi;
   }
   const u64 in_warp = warp_sum_u64(mine);
   const u64 upto = smp_block_scan(sh, lane == 0 ? in_warp : 0ull);
   const u64 warp_end = __shfl_sync(0xffffffffu, upto, 0);
-  if (tid == kSmpThreads - 1) sh->ties[which] = upto;
-  if (tid == 0) sh->border[which] = 0;
+  if (tid == kSmpThreads - 1)
+    for (int k = 0; k < r.ranks; ++k) st_peer_u64(&sh->ties_in[which][r.rank], k, upto);
   cluster_sync();
-  u64 before = 0;
-  for (int k = 0; k < r.rank; ++k) before += ld_peer_u64(&sh->ties[which], k);
-  u64 at = before + warp_end - in_warp;
+  const u64 n_keep = sh->n_keep;
+  u64 at = warp_end - in_warp;
+  for (int k = 0; k < r.rank; ++k) at += sh->ties_in[which][k];
   if (at < n_keep && n_keep <= at + in_warp) {
     for (int i0 = beg; i0 < end; i0 += 32) {
       const int i = i0 + lane;
-      const u64 key = i < end ? smp_key(r.x[i], r.begin + i) : 0ull;
+      const u64 key = i < end ? smp_key(smp_norm(__ldg(r.x + i)), r.begin + i) : 0ull;
       const bool tie = i < end && key >= tie_lo && key <= tie_hi;
       const unsigned b = __ballot_sync(0xffffffffu, tie);
       const u64 rank_here = at + __popc(b & ((1u << lane) - 1)) + 1;
-      if (tie && rank_here == n_keep) sh->border[which] = key;
+      if (tie && rank_here == n_keep)
+        for (int k = 0; k < r.ranks; ++k) st_peer_u64(&sh->border[which], k, key);
       at += __popc(b);
     }
   }
   cluster_sync();
-  u64 key = 0;
-  for (int k = 0; k < r.ranks; ++k) key = max(key, ld_peer_u64(&sh->border[which], k));
-  return key;
+  return sh->border[which];
+}
+
+// The same by histograms of linear bins: of what lies below the maximum, then
+// of the bin in which the border lies if it holds more than a list; the tokens
+// of the last bin are gathered and sorted.  Falls back to the radix search where
+// even that holds too many (ties).
+__device__ __noinline__ u64 smp_border(const SmpRow& r, float scale, bool by_mass, u64 floor_key,
+                                       u64 want, double top_p, int which) {
+  SmpShared* sh = r.sh;
+  const int tid = threadIdx.x;
+  if (!r.fast) return smp_border_radix(r, by_mass, floor_key, want, top_p, which);
+  const float tau = floor_key ? smp_key_value(floor_key) : -INFINITY;
+  const int last = floor_key ? static_cast<int>(smp_id(floor_key)) - r.begin : 0x7fffffff;
+  unsigned bin = 0;
+  float shift = 0.f;         // second level: (m - x) scale - shift spans [0, 1]
+  u64 base = 0;              // rank 0
+  double goal = static_cast<double>(want);
+  // bin of x at a level; kSmpBins or more: not looked at
+  auto bin_at = [&](int level, float x, int i) -> unsigned {
+    unsigned b = smp_bin(r.m, scale, x);
+    if (level) {
+      if (b != bin) return kSmpBins;
+      const float f = fmaxf(fmaf(r.m - x, scale, -shift), 0.f);
+      b = min(__float_as_uint(fmaf(f, kSmpBins - 2.f, 8388608.f)) - 0x4B000000u,
+              kSmpBins - 1u);
+    }
+    return x > tau || (x == tau && i <= last) ? b : kSmpBins;
+  };
+  unsigned sub = 0;
+  int level = 0;
+  constexpr u64 kRefine = 1ull << 32, kNothing = 2ull << 32;
+  for (;; ++level) {
+    smp_clear(sh, kSmpBins, by_mass);
+    for (int i0 = tid * 4; i0 < r.padded; i0 += kSmpThreads * 4) {
+      const float4 x4 = smp_load4(r, i0);
+      const float xs[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const unsigned b = bin_at(level, xs[q], i0 + q);
+        if (b >= kSmpBins) continue;
+        u64 w = 0;
+        if (by_mass && (w = smp_weight(r, xs[q])) == 0) continue;
+        smp_count(sh, b, by_mass, w);
+      }
+    }
+    cluster_sync();
+    if (r.rank == 0) {
+      const SmpHit h = smp_merge<kSmpBins>(r, by_mass, false, base,
+                                           by_mass && level == 0 ? top_p : -1.0, goal);
+      base = h.base;
+      // fewer than wanted weigh anything: nothing to cut
+      const bool nothing = level == 0 && (h.all == 0 || (!by_mass && h.all < want));
+      smp_tell(r, nothing ? kNothing : h.cnt > kSmpList ? kRefine | h.bin : h.bin);
+    }
+    if (tid == 0) sh->n_own = 0;
+    cluster_sync();
+    const u64 told = sh->told;
+    sub = static_cast<unsigned>(told);
+    if (told >= kNothing) return floor_key;
+    if (told < kRefine) break;
+    if (level) return smp_border_radix(r, by_mass, floor_key, want, top_p, which);
+    bin = sub;
+    shift = static_cast<float>(sub) - 0.5f;
+  }
+  for (int i0 = tid * 4; i0 < r.padded; i0 += kSmpThreads * 4) {
+    const float4 x4 = smp_load4(r, i0);
+    const float xs[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (bin_at(level, xs[q], i0 + q) == sub) smp_candidate(sh, xs[q], r.begin + i0 + q);
+  }
+  smp_hand_over(sh, 1 + which);
+  cluster_sync();
+  if (r.rank == 0) {
+    const int n = min(sh->n_list[1 + which], static_cast<unsigned>(kSmpList));
+    smp_sort(sh->list, n);
+    constexpr int kPer = kSmpList / kSmpThreads;
+    const int i0 = kPer * tid;
+    u64 w[kPer], sum = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      w[q] = i0 + q < n ? (by_mass ? smp_weight(r, smp_key_value(sh->list[i0 + q])) : 1ull) : 0ull;
+      sum += w[q];
+    }
+    u64 at = base + smp_block_scan(sh, sum) - sum;
+    if (tid == 0) sh->first_bad = 0;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      if (w[q] && static_cast<double>(at) < goal) atomicMax(&sh->first_bad, i0 + q);
+      at += w[q];
+    }
+    __syncthreads();
+    if (tid < r.ranks) st_peer_u64(&sh->border[which], tid, sh->list[sh->first_bad]);
+  }
+  cluster_sync();
+  return sh->border[which];
 }
 
 struct SmpResult {
@@ -356,55 +604,77 @@ struct SmpResult {
 __device__ __forceinline__ float smp_unit(float u) {   // into [0, 1)
   return u > 0.f ? fminf(u, 0.99999994f) : 0.f;
 }
+__device__ __forceinline__ bool smp_accepts(u64 draft_w, u64 total, float u_accept) {
+  return draft_w > 0 && (draft_w == total || static_cast<double>(u_accept) *
+                                                     static_cast<double>(total) <
+                                                 static_cast<double>(draft_w));
+}
+__device__ __forceinline__ float smp_share(u64 w, u64 total) {
+  return static_cast<float>(static_cast<double>(w) / static_cast<double>(total));
+}
 
 // Draw from the tokens with key >= floor_key in vocabulary order, over all of
 // the row.  draft >= 0: first offered for acceptance with u_accept.
-__device__ SmpResult smp_draw_row(const SmpRow& r, u64 floor_key, int draft, float u_accept,
-                                  float u) {
+__device__ __forceinline__ SmpResult smp_draw_row(const SmpRow& r, u64 floor_key, int draft,
+                                                  float u_accept, float u) {
   SmpShared* sh = r.sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int seg = ((r.len + kSmpWarps - 1) / kSmpWarps + 31) / 32 * 32;
-  const int beg = min(r.len, warp * seg), end = min(r.len, beg + seg);
+  const float tau = floor_key ? smp_key_value(floor_key) : -INFINITY;
+  const int last = floor_key ? static_cast<int>(smp_id(floor_key)) - r.begin : 0x7fffffff;
+  // kept: above the border's value, or at it and not behind its id
+  auto weight = [&](float x, int i) -> u64 {
+    return x > tau || (x == tau && i <= last) ? smp_weight(r, x) : 0ull;
+  };
+  // warps own runs of 128-token groups, a lane four neighbours of a group
+  const int seg = ((r.padded >> 7) + kSmpWarps - 1) / kSmpWarps * 128;
+  const int beg = min(r.padded, warp * seg), end = min(r.padded, beg + seg);
   const int draft_at = draft - r.begin;
-  u64 mine = 0, dw = 0;
-  for (int i = beg + lane; i < end; i += 32) {
-    const float x = r.x[i];
-    if (smp_key(x, r.begin + i) < floor_key) continue;
-    const u64 w = smp_weight(r, x);
-    mine += w;
-    if (i == draft_at) dw = w;
+  u64 mine = 0;
+  if (floor_key == 0 && r.fast && r.w_min == 0) {
+#pragma unroll 2
+    for (int i = beg + lane * 4; i < end; i += 128) {
+      const float4 v = smp_load4(r, i);
+      mine += smp_bits(r, v.x) + smp_bits(r, v.y);
+      mine += smp_bits(r, v.z) + smp_bits(r, v.w);
+    }
+    mine -= static_cast<u64>((end - beg) / 32) * kSmpBias;
+  } else {
+    for (int i = beg + lane * 4; i < end; i += 128) {
+      const float4 v = smp_load4(r, i);
+      mine += weight(v.x, i) + weight(v.y, i + 1) + weight(v.z, i + 2) + weight(v.w, i + 3);
+    }
   }
   const u64 in_warp = warp_sum_u64(mine);
-  dw = warp_sum_u64(dw);
-  if (tid == 0) sh->draft_w = 0;
   const u64 upto = smp_block_scan(sh, lane == 0 ? in_warp : 0ull);
-  if (lane == 0 && dw) sh->draft_w = dw;
-  if (tid == kSmpThreads - 1) sh->kept = upto;
-  cluster_sync();
+  if (tid == kSmpThreads - 1) {
+    const u64 d = draft >= 0 && draft_at >= 0 && draft_at < r.len
+                      ? weight(__ldg(r.x + draft_at), draft_at)
+                      : 0ull;
+    for (int k = 0; k < r.ranks; ++k) {
+      st_peer_u64(&sh->kept_in[r.rank], k, upto);
+      st_peer_u64(&sh->draft_in[r.rank], k, d);
+    }
+  }
+  if (tid == 0) sh->first_bad = kSmpWarps;
+  cluster_sync();   // the row's last: no CTA touches another's memory behind it
   u64 before = 0, total = 0, draft_w = 0;
   int draft_rank = -1;
   for (int k = 0; k < r.ranks; ++k) {
-    const u64 s = ld_peer_u64(&sh->kept, k);
-    const u64 d = ld_peer_u64(&sh->draft_w, k);
+    const u64 s = sh->kept_in[k], d = sh->draft_in[k];
     if (k < r.rank) before += s;
     total += s;
     draft_w += d;
     if (d) draft_rank = k;
   }
-  cluster_sync();   // no CTA leaves while another reads its shared memory
   SmpResult out = {0, 0, -1, 0.f};
-  if (draft >= 0 && draft_w > 0 &&
-      (draft_w == total ||
-       static_cast<double>(u_accept) * static_cast<double>(total) < static_cast<double>(draft_w))) {
+  if (smp_accepts(draft_w, total, u_accept)) {
     out.writer = r.rank == 0 && tid == 0;
     out.accepted = 1;
     out.token = draft;
     return out;
   }
-  if (draft >= 0) {
-    total -= draft_w;
-    if (draft_rank >= 0 && draft_rank < r.rank) before -= draft_w;
-  }
+  total -= draft_w;
+  if (draft_rank >= 0 && draft_rank < r.rank) before -= draft_w;
   if (total == 0) {
     out.writer = r.rank == 0 && tid == 0;
     return out;
@@ -413,308 +683,449 @@ __device__ SmpResult smp_draw_row(const SmpRow& r, u64 floor_key, int draft, flo
   // the warp in whose run the running sum passes the goal
   const u64 warp_all = __shfl_sync(0xffffffffu, upto, 0);
   u64 end_sum = before + warp_all, run = end_sum - in_warp;
-  if (draft >= 0 && draft_rank == r.rank) {
+  if (draft_rank == r.rank) {
     if (draft_at < beg) run -= draft_w;
     if (draft_at < end) end_sum -= draft_w;
   }
-  if (static_cast<double>(run) > goal || static_cast<double>(end_sum) <= goal || run == end_sum)
-    return out;
-  for (int i0 = beg; i0 < end; i0 += 32) {
-    const int i = i0 + lane;
-    u64 w = 0;
-    if (i < end && (draft < 0 || i != draft_at)) {
-      const float x = r.x[i];
-      if (smp_key(x, r.begin + i) >= floor_key) w = smp_weight(r, x);
+  if (lane == 0 && run != end_sum && !(static_cast<double>(run) > goal) &&
+      static_cast<double>(end_sum) > goal) {
+    sh->first_bad = warp;
+    sh->bcast[0] = run;
+  }
+  __syncthreads();
+  if (sh->first_bad >= kSmpWarps) return out;    // not in this slice
+  // the CTA scans that run together, eight neighbours a thread
+  const int b0 = static_cast<int>(sh->first_bad) * seg, b1 = min(r.padded, b0 + seg);
+  run = sh->bcast[0];
+  for (int i0 = b0; i0 < b1; i0 += kSmpThreads * 4) {
+    const int i = i0 + tid * 4;
+    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (i < b1) {
+      const float4 v = smp_load4(r, i);
+      x[0] = v.x;
+      x[1] = v.y;
+      x[2] = v.z;
+      x[3] = v.w;
     }
-    const u64 upto_i = run + warp_scan_u64(w, lane);
-    const unsigned b = __ballot_sync(0xffffffffu, static_cast<double>(upto_i) > goal);
-    if (b) {
-      if (lane == __ffs(b) - 1) {
+    u64 w[4], sum = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      w[q] = i >= b1 || (draft_w && draft_rank == r.rank && i + q == draft_at)
+                 ? 0ull
+                 : weight(x[q], i + q);
+      sum += w[q];
+    }
+    u64 at = run + smp_block_scan(sh, sum);
+    if (tid == kSmpThreads - 1) sh->bcast[1] = at;
+    at -= sum;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (w[q] && !(static_cast<double>(at) > goal) && static_cast<double>(at + w[q]) > goal) {
         out.writer = 1;
-        out.token = r.begin + i;
-        out.prob = static_cast<float>(static_cast<double>(w) / static_cast<double>(total));
+        out.token = r.begin + i + q;
+        out.prob = smp_share(w[q], total);
       }
-      return out;
+      at += w[q];
     }
-    run = __shfl_sync(0xffffffffu, upto_i, 31);
+    __syncthreads();
+    run = sh->bcast[1];
   }
   return out;
 }
 
 // The same from n candidates in rank 0's list (keys in any order; every token
 // that is kept is among them).  mass_all: the weight that top_p refers to, 0:
-// that of the candidates.  Called by every thread of rank 0.
-__device__ SmpResult smp_draw_list(const SmpRow& r, int n, int k, double top_p, u64 mass_all,
-                                   int draft, float u_accept, float u) {
+// that of the first k candidates.  Called by every thread of rank 0.
+__device__ __forceinline__ SmpResult smp_draw_few(const SmpRow& r, int n, int k, double top_p,
+                                                  u64 mass_all, int draft, float u_accept,
+                                                  float u) {
+  // n <= kSmpFew: kShare threads compare a candidate with all others, so its
+  // place, and the weight before it in either order, need no sort
   SmpShared* sh = r.sh;
   const int tid = threadIdx.x;
+  constexpr int kShare = kSmpThreads / kSmpFew;
+  const int i = tid / kShare, q0 = tid % kShare;
   SmpResult out = {0, 0, -1, 0.f};
-  int n2 = 32;
-  while (n2 < n) n2 <<= 1;
-  for (int i = n + tid; i < n2; i += kSmpThreads) sh->list[i] = 0;
-  smp_sort(sh->list, n2);
-  if (tid == 0) {
-    sh->first_bad = n;
-    sh->draft_w = 0;
-  }
-  // running weights in falling order: two neighbours a thread
-  const int i0 = 2 * tid;
-  u64 w[2] = {0, 0};
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int i = i0 + q;
-    if (i < n && (k <= 0 || i < k))
-      w[q] = smp_weight(r, smp_value(static_cast<uint32_t>(sh->list[i] >> 32)));
-  }
-  u64 run = smp_block_scan(sh, w[0] + w[1]);
-  if (tid == kSmpThreads - 1) sh->bcast[0] = run;
+  if (tid < n) sh->w[tid] = smp_weight(r, smp_key_value(sh->list[tid]));
   __syncthreads();
-  run -= w[0] + w[1];
-  const double goal =
-      top_p * static_cast<double>(mass_all ? mass_all : sh->bcast[0]);
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int i = i0 + q;
-    if (i < n && i > 0 && (w[q] == 0 || !(static_cast<double>(run) < goal)))
-      atomicMin(&sh->first_bad, static_cast<unsigned>(i));
-    run += w[q];
-    if (i < n) sh->w[i] = w[q];
-  }
-  __syncthreads();
-  n = sh->first_bad;            // the kept tokens are list[0 .. n)
-  n2 = 32;
-  while (n2 < n) n2 <<= 1;
-  // into vocabulary order, each with its place in w
-  u64 key[2];
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int i = i0 + q;
-    key[q] = 0;
-    if (i < n) {
-      const uint32_t id = smp_id(sh->list[i]);
-      key[q] = (static_cast<u64>(0xffffffffu - id) << 32) | static_cast<u64>(i);
-      if (static_cast<int>(id) == draft) sh->draft_w = w[q];
+  const u64 key = i < n ? sh->list[i] : 0ull;
+  u64 w = i < n ? sh->w[i] : 0ull, before = 0;
+  int place = 0;
+  for (int j = q0; j < n; j += kShare)
+    if (sh->list[j] > key) {
+      ++place;
+      before += sh->w[j];
     }
+#pragma unroll
+  for (int o = 1; o < kShare; o <<= 1) {
+    place += __shfl_xor_sync(0xffffffffu, place, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
   }
+  if (k <= 0 || k > n) k = n;
+  if (i < n && q0 == 0 && place == k - 1) sh->bcast[0] = before + w;
   __syncthreads();
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-    if (i0 + q < n2) sh->list[i0 + q] = key[q];
-  smp_sort(sh->list, n2);
-  const u64 draft_w = sh->draft_w;
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int i = i0 + q;
-    key[q] = i < n ? sh->list[i] : 0;
-    w[q] = i < n ? sh->w[static_cast<uint32_t>(key[q])] : 0;
+  const double goal = top_p * static_cast<double>(mass_all ? mass_all : sh->bcast[0]);
+  if (place >= k || (place > 0 && !(static_cast<double>(before) < goal))) w = 0;
+  if (i < n && q0 == 0) sh->w[i] = w;
+  __syncthreads();
+  const uint32_t id = smp_id(key);
+  u64 total = 0, draft_w = 0;
+  before = 0;
+  for (int j = q0; j < n; j += kShare) {
+    const u64 wj = sh->w[j];
+    const uint32_t idj = smp_id(sh->list[j]);
+    total += wj;
+    if (static_cast<int>(idj) == draft) draft_w += wj;
+    else if (idj < id) before += wj;
   }
-  u64 total = smp_block_sum(sh, w[0] + w[1]);
-  if (draft >= 0 && draft_w > 0 &&
-      (draft_w == total ||
-       static_cast<double>(u_accept) * static_cast<double>(total) < static_cast<double>(draft_w))) {
+#pragma unroll
+  for (int o = 1; o < kShare; o <<= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    draft_w += __shfl_xor_sync(0xffffffffu, draft_w, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if (smp_accepts(draft_w, total, u_accept)) {
     out.writer = tid == 0;
     out.accepted = 1;
     out.token = draft;
     return out;
   }
-  int id[2];
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    id[q] = static_cast<int>(0xffffffffu - static_cast<uint32_t>(key[q] >> 32));
-    if (i0 + q < n && id[q] == draft) w[q] = 0;
-  }
-  if (draft >= 0) total -= draft_w;
+  total -= draft_w;
   if (total == 0) {
     out.writer = tid == 0;
     return out;
   }
   const double at = static_cast<double>(smp_unit(u)) * static_cast<double>(total);
-  run = smp_block_scan(sh, w[0] + w[1]) - w[0] - w[1];
+  if (i < n && q0 == 0 && w && static_cast<int>(id) != draft &&
+      !(static_cast<double>(before) > at) && static_cast<double>(before + w) > at) {
+    out.writer = 1;
+    out.token = static_cast<int>(id);
+    out.prob = smp_share(w, total);
+  }
+  return out;
+}
+__device__ __noinline__ SmpResult smp_draw_list(const SmpRow& r, int n, int k, double top_p,
+                                                u64 mass_all, int draft, float u_accept, float u) {
+  SmpShared* sh = r.sh;
+  const int tid = threadIdx.x;
+  constexpr int kPer = kSmpList / kSmpThreads;
+  SmpResult out = {0, 0, -1, 0.f};
+  smp_sort(sh->list, n);
+  if (tid == 0) {
+    sh->first_bad = n;
+    sh->bcast[2] = 0;
+  }
+  // running weights in falling order: neighbours a thread
+  const int i0 = kPer * tid;
+  u64 w[kPer], sum = 0;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    if (!(static_cast<double>(run) > at) && static_cast<double>(run + w[q]) > at) {
+  for (int q = 0; q < kPer; ++q) {
+    const int i = i0 + q;
+    w[q] = i < n && (k <= 0 || i < k) ? smp_weight(r, smp_key_value(sh->list[i])) : 0ull;
+    sum += w[q];
+  }
+  u64 run = smp_block_scan(sh, sum);
+  if (tid == kSmpThreads - 1) sh->bcast[0] = run;
+  __syncthreads();
+  run -= sum;
+  const double goal = top_p * static_cast<double>(mass_all ? mass_all : sh->bcast[0]);
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int i = i0 + q;
+    if (i < n && i > 0 && (w[q] == 0 || !(static_cast<double>(run) < goal)))
+      atomicMin(&sh->first_bad, static_cast<unsigned>(i));
+    run += w[q];
+  }
+  __syncthreads();
+  n = sh->first_bad;            // the kept tokens are list[0 .. n)
+  // into vocabulary order
+  u64 key[kPer];
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int i = i0 + q;
+    key[q] = 0;
+    if (i < n) {
+      const u64 old = sh->list[i];
+      if (static_cast<int>(smp_id(old)) == draft) sh->bcast[2] = w[q];
+      key[q] = (old << 32) | (old >> 32);     // falling ~id first
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kPer; ++q)
+    if (i0 + q < n) sh->list[i0 + q] = key[q];
+  smp_sort(sh->list, n);
+  const u64 draft_w = sh->bcast[2];
+  int id[kPer];
+  sum = 0;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int i = i0 + q;
+    key[q] = i < n ? sh->list[i] : 0;
+    id[q] = static_cast<int>(0xffffffffu - static_cast<uint32_t>(key[q] >> 32));
+    w[q] = i < n ? smp_weight(r, smp_value(static_cast<uint32_t>(key[q]))) : 0;
+    if (id[q] == draft) w[q] = 0;
+    sum += w[q];
+  }
+  run = smp_block_scan(sh, sum);
+  if (tid == kSmpThreads - 1) sh->bcast[1] = run;
+  __syncthreads();
+  const u64 total = sh->bcast[1];             // without the draft
+  if (smp_accepts(draft_w, total + draft_w, u_accept)) {
+    out.writer = tid == 0;
+    out.accepted = 1;
+    out.token = draft;
+    return out;
+  }
+  if (total == 0) {
+    out.writer = tid == 0;
+    return out;
+  }
+  run -= sum;
+  const double at = static_cast<double>(smp_unit(u)) * static_cast<double>(total);
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    if (w[q] && !(static_cast<double>(run) > at) && static_cast<double>(run + w[q]) > at) {
       out.writer = 1;
       out.token = id[q];
-      out.prob = static_cast<float>(static_cast<double>(w[q]) / static_cast<double>(total));
+      out.prob = smp_share(w[q], total);
     }
     run += w[q];
   }
   return out;
 }
 
-// One row: copy, filters, draw.  Exactly one thread of the cluster returns with
+// One row: maxima, filters, draw.  Exactly one thread of the cluster returns with
 // writer set.
-__device__ SmpResult smp_row(SmpShared* sh, float* xs, const float* row, int V, int slice,
-                             const SampleSettings& set, int at, int draft, float u_accept,
-                             float u) {
+__device__ __forceinline__ SmpResult smp_row(SmpShared* sh, const float* row, int V, int slice,
+                                             const SampleSettings& set, int at, int draft,
+                                             float u_accept, float u) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   SmpRow r;
   r.sh = sh;
-  r.x = xs;
   r.rank = static_cast<int>(cluster_rank());
   r.ranks = gridDim.x;
   r.begin = r.rank * slice;
   r.len = max(0, min(V - r.begin, slice));
-  const float* src = row + r.begin;
-  if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-    for (int i = tid * 4; i + 4 <= r.len; i += kSmpThreads * 4) cp_async16(xs + i, src + i);
-    for (int i = (r.len & ~3) + tid; i < r.len; i += kSmpThreads) cp_async4(xs + i, src + i);
-  } else {
-    for (int i = tid; i < r.len; i += kSmpThreads) cp_async4(xs + i, src + i);
-  }
+  r.padded = (r.len + 127) & ~127;
+  r.x = row + r.begin;
+  r.wide = (reinterpret_cast<uintptr_t>(r.x) & 15) == 0;
   const float T = set.temperature ? set.temperature[at] : 1.f;
   const int k_in = set.top_k ? set.top_k[at] : 0;
   const float p_in = set.top_p ? set.top_p[at] : 1.f;
   const float m_in = set.min_p ? set.min_p[at] : 0.f;
-  if (tid < 32) sh->tab[tid] = exp2(tid / 32.0);
-  for (int i = tid; i < kSmpBins; i += kSmpThreads) sh->cnt[i] = 0;
-  cp_async_wait_all();
-  __syncthreads();
-  // largest (value, id) and smallest finite value
-  float bv = -INFINITY, lo = INFINITY;
-  int bi = -1;
-  for (int i = tid; i < r.len; i += kSmpThreads) {
-    float x = xs[i];
-    x = x != x ? -INFINITY : x + 0.f;
-    xs[i] = x;
-    if (x > bv) {
-      bv = x;
-      bi = i;
-    }
-    if (x > -INFINITY) lo = fminf(lo, x);
-  }
-  u64 key = bi >= 0 ? smp_key(bv, r.begin + bi) : 0ull;
+  // the largest of this thread's tokens (a NaN never is); eight loads in flight
+  float mine = -INFINITY;
+  for (int i0 = tid * 4; i0 < r.padded; i0 += kSmpThreads * 32) {
+    float4 v[8];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const u64 other = __shfl_xor_sync(0xffffffffu, key, o);
-    key = other > key ? other : key;
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-  }
-  if (lane == 0) {
-    sh->warp_a[warp] = key;
-    reinterpret_cast<float*>(sh->mass)[warp] = lo;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kSmpWarps; ++w) {
-      key = max(key, sh->warp_a[w]);
-      lo = fminf(lo, reinterpret_cast<float*>(sh->mass)[w]);
+    for (int q = 0; q < 8; ++q) {
+      const int i = i0 + q * kSmpThreads * 4;
+      v[q] = i < r.padded ? smp_load4(r, i)
+                          : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     }
-    sh->top_key = key;
-    sh->low = lo;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      mine = fmaxf(mine, fmaxf(fmaxf(v[q].x, v[q].y), fmaxf(v[q].z, v[q].w)));
+  }
+  const bool greedy = !(T > 0.f);
+  const bool by_k = k_in > 0 && k_in < V;
+  const bool by_p = p_in < 1.f;
+  const double top_p = p_in > 0.f ? static_cast<double>(p_in) : 0.0;
+  const float scale = fminf((kSmpBins - 1) / (kSmpReach * T), 3e38f);
+  const bool by_list = !greedy && (by_k ? k_in <= kSmpListTopK : by_p);
+  if (!greedy) {
+    for (int i = tid; i < kSmpTab; i += kSmpThreads) sh->tab[i] = exp2(i * (1.0 / kSmpTab));
+    if (by_list)
+      for (int i = tid; i < kSmpBins; i += kSmpThreads) sh->cnt[i] = 0;
+  }
+  if (tid < 3) sh->n_list[tid] = 0;
+  if (tid < 4) sh->thr[tid] = -INFINITY;
+  if (tid == 0) {
+    sh->n_own = 0;
+    sh->first = 0xffffffffu;
+  }
+  float top = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float* warp_f = reinterpret_cast<float*>(sh->warp_a);
+  if (lane == 0) warp_f[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSmpWarps; ++w) top = fmaxf(top, warp_f[w]);
+  if (by_list) {
+    // thr[j]: a value that at least aim / 2^j of the slice's tokens reach, seen
+    // from the threads' maxima alone (-inf where too few are within reach)
+    const unsigned b = smp_bin(top, scale, mine);
+    if (b < kSmpBins) atomicAdd(&sh->cnt[b], 1u);
+    __syncthreads();
+    constexpr int kPer = kSmpBins / kSmpThreads;
+    unsigned c[kPer], sum = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      c[q] = sh->cnt[tid * kPer + q];
+      sum += c[q];
+    }
+    unsigned run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned w = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += w;
+    }
+    unsigned* warp_u = reinterpret_cast<unsigned*>(sh->bcast);
+    if (lane == 31) warp_u[warp] = run;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSmpWarps; ++w)
+      if (w < warp) run += warp_u[w];
+    run -= sum;
+    const unsigned aim = by_k ? static_cast<unsigned>(k_in) : static_cast<unsigned>(kSmpAim);
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const unsigned need = (aim + (1u << j) - 1) >> j;
+        // below every value of that bin, whatever its rounding
+        if (run < need && run + c[q] >= need)
+          sh->thr[j] = __double2float_rd(static_cast<double>(top) -
+                                         (tid * kPer + q + 0.51) / static_cast<double>(scale));
+      }
+      run += c[q];
+    }
+    __syncthreads();
+  }
+  if (tid < r.ranks) {
+    st_peer_u32(&sh->top_in[r.rank], tid, __float_as_uint(top));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      st_peer_u32(&sh->thr_in[r.rank][j], tid, __float_as_uint(sh->thr[j]));
   }
   cluster_sync();
-  key = 0;
-  lo = INFINITY;
-  for (int k = 0; k < r.ranks; ++k) {
-    key = max(key, ld_peer_u64(&sh->top_key, k));
-    lo = fminf(lo, __uint_as_float(ld_peer_u32(&sh->low, k)));
+  // 2^j slices that hold aim / 2^j tokens each from a value on hold aim: the
+  // 2^j-th largest of thr[j]; of the four such values the largest
+  float cut = -INFINITY;
+  {
+    const int c = lane >> 2, j = lane & 3;
+    top = lane < r.ranks ? sh->top_in[lane] : -INFINITY;
+    if (by_list) {
+      const float v = c < r.ranks ? sh->thr_in[c][j] : -INFINITY;
+      int above = 0;
+#pragma unroll
+      for (int o = 1; o < 8; ++o) {
+        const int from = ((c + o) & 7) * 4 + j;
+        const float w = __shfl_sync(0xffffffffu, v, from);
+        above += w > v || (w == v && from < lane);
+      }
+      cut = above == (1 << j) - 1 ? v : -INFINITY;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, o));
+    }
   }
+  r.m = top + 0.f;
   SmpResult out = {r.rank == 0 && tid == 0, 0, -1, 0.f};
-  if (key == 0) {              // nothing but -inf and NaN
+  if (top == -INFINITY) return out;   // nothing but -inf and NaN
+  if (greedy) {                       // the first id of the largest value
+    if (mine == top)
+      for (int i = tid * 4; i < r.padded; i += kSmpThreads * 4) {
+        const float4 v = smp_load4(r, i);
+        const int q = v.x == top ? 0 : v.y == top ? 1 : v.z == top ? 2 : v.w == top ? 3 : -1;
+        if (q >= 0) {
+          atomicMin(&sh->first, static_cast<unsigned>(r.begin + i + q));
+          break;
+        }
+      }
+    __syncthreads();
+    if (tid == 0) st_peer_u32(&sh->first_in[r.rank], 0, sh->first);
     cluster_sync();
-    return out;
-  }
-  r.m = smp_value(static_cast<uint32_t>(key >> 32));
-  if (!(T > 0.f)) {            // greedy
-    cluster_sync();
-    out.token = static_cast<int>(smp_id(key));
+    unsigned id = 0xffffffffu;
+    for (int k = 0; k < r.ranks; ++k) id = min(id, sh->first_in[k]);
+    out.token = static_cast<int>(id);
     out.accepted = out.token == draft;
     out.prob = 1.f;
     return out;
   }
-  r.c = 1.4426950408889634 / static_cast<double>(T);
+  r.md = static_cast<double>(r.m);
+  r.c = kSmpTab * 1.4426950408889634 / static_cast<double>(T);
   r.w_min = m_in > 0.f ? static_cast<u64>(ceil(fmin(m_in, 1.0) * 17592186044416.0)) : 0ull;
-  const bool by_k = k_in > 0 && k_in < V;
-  const bool by_p = p_in < 1.f;
-  const double top_p = p_in > 0.f ? static_cast<double>(p_in) : 0.0;
-  if (!by_k && !by_p) return smp_draw_row(r, 0ull, draft, u_accept, u);
-  // How many tokens lie how far below the largest: linear bins of m - x down to
-  // where a token weighs nothing.  s m - s x rounds monotonely, so each bin
-  // holds a run of the falling order.
-  const float reach = fminf(kSmpReach * T, r.m - lo);
-  const float scale = (kSmpBins - 0.5f) / fmaxf(reach, 1e-30f);
-  auto bin_of = [&](float x) {   // kSmpBins: too far down
-    const float d = x == r.m ? 0.f : (r.m - x) * scale;
-    return d < static_cast<float>(kSmpBins) ? static_cast<int>(d) : kSmpBins;
-  };
-  for (int i = tid; i < r.len; i += kSmpThreads) {
-    const int b = bin_of(xs[i]);
-    if (b < kSmpBins) atomicAdd(&sh->cnt[b], 1u);
-  }
-  // top_p without top_k: the weight it refers to is the whole row's
-  u64 mass_all = 0;
-  if (!by_k) {
-    u64 mine = 0;
-    for (int i = tid; i < r.len; i += kSmpThreads) mine += smp_weight(r, xs[i]);
-    mine = smp_block_sum(sh, mine);
-    if (tid == 0) sh->mass_all = mine;
-  }
-  cluster_sync();
-  if (!by_k)
-    for (int k = 0; k < r.ranks; ++k) mass_all += ld_peer_u64(&sh->mass_all, k);
-  // the first bin by which every kept token has come: top_k tokens, or top_p
-  // of the weight even if every token of a bin weighs as little as its far edge
-  // (whose rounding, 46 bits times 2^-22, the factor 1.0001 covers)
-  u64 c[2] = {0, 0}, earlier[2] = {0, 0};
-  const double edge = -r.c / static_cast<double>(scale);
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-    for (int k = 0; k < r.ranks; ++k) {
-      const u64 v = ld_peer_u32(&sh->cnt[2 * tid + q], k);
-      c[q] += v;
-      if (k < r.rank) earlier[q] += v;
+  r.x_cut = __double2float_rd(r.md - 46.5 * kSmpTab / r.c);
+  const double below = (r.md - static_cast<double>(r.x_cut)) * r.c;
+  r.fast = r.x_cut > -INFINITY && r.m < INFINITY && below >= 46.0 * kSmpTab &&
+           below <= 60.0 * kSmpTab;
+  if (by_list && r.fast) {
+    // tokens further down than x_cut weigh nothing
+    const bool whole = !(cut > r.x_cut);
+    cut = fmaxf(cut, r.x_cut);
+    u64 mass = 0;
+    if (by_k) {
+      if (mine >= cut)
+        for (int i = tid * 4; i < r.padded; i += kSmpThreads * 4) {
+          const float4 v = smp_load4(r, i);
+          if (v.x >= cut) smp_candidate(sh, v.x, r.begin + i);
+          if (v.y >= cut) smp_candidate(sh, v.y, r.begin + i + 1);
+          if (v.z >= cut) smp_candidate(sh, v.z, r.begin + i + 2);
+          if (v.w >= cut) smp_candidate(sh, v.w, r.begin + i + 3);
+        }
+    } else {                 // top_p refers to the whole row's weight
+#pragma unroll 2
+      for (int i = tid * 4; i < r.padded; i += kSmpThreads * 4) {
+        const float4 v = smp_load4(r, i);
+        if (fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= cut) {
+          if (v.x >= cut) smp_candidate(sh, v.x, r.begin + i);
+          if (v.y >= cut) smp_candidate(sh, v.y, r.begin + i + 1);
+          if (v.z >= cut) smp_candidate(sh, v.z, r.begin + i + 2);
+          if (v.w >= cut) smp_candidate(sh, v.w, r.begin + i + 3);
+        }
+        if (r.w_min) {
+          mass += smp_weight(r, v.x) + smp_weight(r, v.y) + smp_weight(r, v.z) +
+                  smp_weight(r, v.w);
+        } else {
+          mass += smp_bits(r, v.x) + smp_bits(r, v.y);
+          mass += smp_bits(r, v.z) + smp_bits(r, v.w);
+          mass -= 4 * kSmpBias;
+        }
+      }
+      mass = smp_block_sum(sh, mass);
+      if (tid == 0) st_peer_u64(&sh->mass_in[r.rank], 0, mass);
     }
-  const u64 need = static_cast<u64>(by_k ? k_in : 0);
-  u64 upto, measure[2];
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-    measure[q] = by_k ? c[q]
-                      : static_cast<u64>(static_cast<double>(c[q]) *
-                                         exp2(edge * (2 * tid + q + 1.0) + kSmpOneBits));
-  upto = smp_block_scan(sh, measure[0] + measure[1]);
-  const u64 goal = by_k ? need
-                        : static_cast<u64>(top_p * static_cast<double>(mass_all) * 1.0001) + 1;
-  if (tid == 0) sh->first_bad = kSmpBins - 1;
-  __syncthreads();
-  if (upto >= goal) {
-    const int b = upto - measure[1] >= goal ? 2 * tid : 2 * tid + 1;
-    atomicMin(&sh->first_bad, static_cast<unsigned>(b));
-  }
-  __syncthreads();
-  const int last_bin = static_cast<int>(sh->first_bad);
-  u64 in = 0, off = 0;
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-    if (2 * tid + q <= last_bin) {
-      in += c[q];
-      off += earlier[q];
-    }
-  in = smp_block_sum(sh, in);
-  off = smp_block_sum(sh, off);
-  if (in <= kSmpList) {
-    if (tid == 0) sh->n_local = 0;
-    __syncthreads();
-    for (int i = tid; i < r.len; i += kSmpThreads) {
-      const float x = xs[i];
-      if (bin_of(x) <= last_bin) {
-        const u64 at_i = off + atomicAdd(&sh->n_local, 1u);
-        if (at_i < kSmpList) st_peer_u64(&sh->list[at_i], 0, smp_key(x, r.begin + i));
+    smp_hand_over(sh, 0);
+    cluster_sync();
+    if (r.rank == 0) {
+      const int n = sh->n_list[0];
+      bool all_in = n <= kSmpList;
+      u64 mass_all = 0;
+      if (!by_k) {
+        for (int k = 0; k < r.ranks; ++k) mass_all += sh->mass_in[k];
+        if (all_in && !whole) {      // does the list reach top_p of the row's weight?
+          u64 w = 0;
+          for (int i = tid; i < n; i += kSmpThreads)
+            w += smp_weight(r, smp_key_value(sh->list[i]));
+          w = smp_block_sum(sh, w);
+          all_in = static_cast<double>(w) >= top_p * static_cast<double>(mass_all);
+        }
+      }
+      if (tid < r.ranks) st_peer_u32(&sh->verdict, tid, all_in);
+      cluster_sync();
+      if (all_in) {
+        const int k = by_k ? k_in : 0;
+        const double p = by_p ? top_p : 2.0;
+        return n <= kSmpFew ? smp_draw_few(r, n, k, p, mass_all, draft, u_accept, u)
+                            : smp_draw_list(r, n, k, p, mass_all, draft, u_accept, u);
+      }
+    } else {
+      cluster_sync();
+      if (sh->verdict) {
+        out.writer = 0;
+        return out;
       }
     }
-    cluster_sync();
-    if (r.rank != 0) {
-      out.writer = 0;
-      return out;
-    }
-    return smp_draw_list(r, static_cast<int>(in), by_k ? k_in : 0, by_p ? top_p : 2.0, mass_all,
-                         draft, u_accept, u);
   }
-  // too many candidates for one list: exact borders over the whole row
-  cluster_sync();
+  // the whole row, from the exact borders where there are any
   u64 floor_key = 0;
-  if (by_k) floor_key = smp_border(r, false, 0ull, need, 0.0, 0);
-  if (by_p) floor_key = smp_border(r, true, floor_key, 0ull, top_p, 1);
+  if (by_k) floor_key = smp_border(r, scale, false, 0ull, static_cast<u64>(k_in), 0.0, 0);
+  if (by_p) floor_key = smp_border(r, scale, true, floor_key, 0ull, top_p, 1);
   return smp_draw_row(r, floor_key, draft, u_accept, u);
 }
 
@@ -730,14 +1141,13 @@ struct SampleParams {
 };
 
 // Cluster y draws row y's token.
-__global__ void __launch_bounds__(kSmpThreads, 2) sample_kernel(const SampleParams p) {
-  extern __shared__ __align__(16) uint8_t smp_smem[];
+__global__ void __launch_bounds__(kSmpThreads, kSmpCtas) sample_kernel(const SampleParams p) {
+  __shared__ SmpShared shared;
   pdl_trigger();
   pdl_wait();
-  SmpShared* sh = reinterpret_cast<SmpShared*>(smp_smem);
-  float* xs = reinterpret_cast<float*>(smp_smem + (sizeof(SmpShared) + 15) / 16 * 16);
+  SmpShared* sh = &shared;
   const int row = blockIdx.y;
-  const SmpResult res = smp_row(sh, xs, p.logits + static_cast<int64_t>(row) * p.ld, p.V, p.slice,
+  const SmpResult res = smp_row(sh, p.logits + static_cast<int64_t>(row) * p.ld, p.V, p.slice,
                                 p.set, row, -1, 0.f, p.u[row]);
   if (res.writer) {
     p.tokens[row] = res.token;
@@ -758,45 +1168,62 @@ struct VerifySampledParams {
   unsigned* done;         // [B] rows of the request that are settled (zeroed before)
   unsigned* refused;      // [B] K + 1 - (first refused row), 0: none yet (zeroed before)
   int32_t* row_token;     // [B][K + 1] what a row would emit if it is the last
+  int run;                // rows that one cluster settles in turn
 };
 
-// Cluster (y, z) settles row z of request y: rows come in order, so when a late
-// row starts, an earlier one of its request may have refused its draft, and the
-// row has nothing to say.  Whether it looks only decides if work is saved: a
-// request's answer is its first refusing row's, whoever ran.  The cluster that
-// settles a request's last row writes the answer.
-__global__ void __launch_bounds__(kSmpThreads, 2)
+// Cluster (y, z) settles rows [z * run, ..) of request y in turn, until one
+// refuses its draft.  Clusters start in the order of z: when a late one starts,
+// an earlier row of its request may have refused, and its rows have nothing to
+// say.  Whether it looks only decides if work is saved: a request's answer is
+// its first refusing row's, whoever ran.  The cluster that settles a request's
+// last rows writes the answer.
+__global__ void __launch_bounds__(kSmpThreads, kSmpCtas)
 verify_sampled_kernel(const VerifySampledParams p) {
-  extern __shared__ __align__(16) uint8_t smp_smem[];
+  __shared__ SmpShared shared;
   pdl_trigger();
   pdl_wait();
-  SmpShared* sh = reinterpret_cast<SmpShared*>(smp_smem);
-  float* xs = reinterpret_cast<float*>(smp_smem + (sizeof(SmpShared) + 15) / 16 * 16);
-  const int b = blockIdx.y, i = blockIdx.z, K = p.K;
-  // one reading for the whole cluster: rank 0's
-  if (threadIdx.x == 0 && cluster_rank() == 0)
-    sh->n_local = *reinterpret_cast<volatile unsigned*>(p.refused + b);
-  cluster_sync();
-  const int refused = static_cast<int>(ld_peer_u32(&sh->n_local, 0));
-  cluster_sync();
-  SmpResult res = {0, 0, -1, 0.f};
-  if (refused && i > K + 1 - refused) {
-    res.writer = cluster_rank() == 0 && threadIdx.x == 0;
-    res.accepted = 1;      // a row that does not matter
-  } else {
+  SmpShared* sh = &shared;
+  const int b = blockIdx.y, K = p.K;
+  const int first = blockIdx.z * p.run, end = min(K + 1, first + p.run);
+  const bool lead = threadIdx.x == 0 && cluster_rank() == 0;
+  bool needed = true;
+  if (first > 0) {
+    // one reading for the whole cluster: rank 0's
+    if (lead) {
+      const unsigned refused = *reinterpret_cast<volatile unsigned*>(p.refused + b);
+      const unsigned told = !(refused && first > K + 1 - static_cast<int>(refused));
+      for (unsigned k = 0; k < gridDim.x; ++k) st_peer_u32(&sh->verdict, k, told);
+    }
+    cluster_sync();
+    needed = sh->verdict != 0;
+    __syncthreads();
+  }
+  for (int i = first; needed && i < end; ++i) {
     const int draft = i < K ? p.drafts[static_cast<int64_t>(b) * K + i] : -1;
-    res = smp_row(sh, xs, p.logits + (static_cast<int64_t>(b) * (K + 1) + i) * p.ld, p.V, p.slice,
-                  p.set, b, draft, i < K ? p.u_accept[static_cast<int64_t>(b) * K + i] : 0.f,
-                  p.u_sample[b]);
+    const SmpResult res =
+        smp_row(sh, p.logits + (static_cast<int64_t>(b) * (K + 1) + i) * p.ld, p.V, p.slice, p.set,
+                b, draft, i < K ? p.u_accept[static_cast<int64_t>(b) * K + i] : 0.f,
+                p.u_sample[b]);
+    if (res.writer && (!res.accepted || i == K)) {
+      p.row_token[static_cast<int64_t>(b) * (K + 1) + i] = res.token;
+      __threadfence();
+      atomicMax(p.refused + b, static_cast<unsigned>(K + 1 - i));
+      __threadfence();
+    }
+    // whether to go on (an accepted draft's writer is the leader); behind the
+    // barrier the row's stores are out, for the leader to count it as settled
+    if (lead) {
+      const unsigned more = res.writer && res.accepted && i < K;
+      for (unsigned k = 0; k < gridDim.x; ++k) st_peer_u32(&sh->told32, k, more);
+    }
+    cluster_sync();
+    needed = sh->told32 != 0;
+    cluster_sync();      // read by all before anything is written again
   }
-  if (!res.writer) return;
-  if (!res.accepted || i == K) {
-    p.row_token[static_cast<int64_t>(b) * (K + 1) + i] = res.token;
-    __threadfence();
-    atomicMax(p.refused + b, static_cast<unsigned>(K + 1 - i));
-  }
+  if (!lead) return;
   __threadfence();
-  if (atomicAdd(p.done + b, 1u) != static_cast<unsigned>(K)) return;
+  const unsigned mine = static_cast<unsigned>(end - first);
+  if (atomicAdd(p.done + b, mine) + mine != static_cast<unsigned>(K + 1)) return;
   __threadfence();
   const int n = K + 1 - static_cast<int>(*reinterpret_cast<volatile unsigned*>(p.refused + b));
   const int32_t last =
