@@ -309,7 +309,7 @@ dflash_status dflash_sample_tokens(const float* logits, int64_t ld, int rows, in
   p.probs = probs;
   p.err = device_error;
   launch_kc(pdl_default(), pl.ranks, sample_kernel, dim3(pl.ranks, rows), dim3(kSmpThreads),
-            0, st, p);
+            sizeof(SmpShared), st, p);
   return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 
@@ -361,7 +361,7 @@ dflash_status dflash_verify_sampled(const int32_t* drafts, const float* target_l
   // so that the ones behind a refused draft cost no launch.
   p.run = std::max(1, std::min(8, B * (K + 1) / 96));
   launch_kc(pdl_default(), pl.ranks, verify_sampled_kernel, dim3(pl.ranks, B, cdiv(K + 1, p.run)),
-            dim3(kSmpThreads), 0, st, p);
+            dim3(kSmpThreads), sizeof(SmpShared), st, p);
   return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 

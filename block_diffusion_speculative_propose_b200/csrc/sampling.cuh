@@ -41,7 +41,6 @@ constexpr int kSmpRadix = 2048;       // bins of a radix level (11 bits)
 constexpr int kSmpList = 1024;        // candidates that one CTA sorts
 constexpr int kSmpFew = 128;          // candidates that are ranked by comparing all pairs
 constexpr int kSmpListTopK = 640;     // largest top_k whose candidates are gathered by maxima
-constexpr int kSmpAim = 512;          // candidates gathered for a top_p alone
 constexpr int kSmpOneBits = 44;       // W of the largest weight: 2^44
 constexpr float kSmpReach = 31.9f;    // 46 ln 2: tokens further below weigh nothing
 constexpr int kSmpTab = 512;          // 2^(j / 512)
@@ -61,8 +60,7 @@ struct SampleSettings {
 struct SmpShared {
   double tab[kSmpTab];
   u64 warp_a[kSmpWarps];             // block-wide sums
-  u64 bcast[4];
-  u64 mass_in[kSmpMaxCluster];       // from each rank: the weight of its slice
+  u64 bcast[5];
   u64 kept_in[kSmpMaxCluster];       // from each rank: its kept weight, the draft's
   u64 draft_in[kSmpMaxCluster];
   u64 ties_in[2][kSmpMaxCluster];    // from each rank: ties of the border value (two searches)
@@ -73,7 +71,7 @@ struct SmpShared {
   float thr[4];
   unsigned first_in[kSmpMaxCluster]; // greedy: the first id that holds the largest value
   unsigned first;
-  unsigned n_list[3];                // rank 0: candidates gathered (three lists)
+  unsigned n_list[4];                // rank 0: candidates gathered (four lists)
   unsigned n_own, own_at;            // this CTA's share of them, its place
   unsigned verdict, told32;          // from rank 0
   unsigned first_bad;
@@ -162,9 +160,14 @@ __device__ __forceinline__ u64 warp_scan_u64(u64 v, int lane) {   // inclusive
   return v;
 }
 
+// The block's shared memory, in a form from which every function sees that it is shared.
+__device__ __forceinline__ SmpShared* smp_shared() {
+  extern __shared__ __align__(16) uint8_t smp_smem[];
+  return reinterpret_cast<SmpShared*>(smp_smem);
+}
+
 // One row as the cluster's threads see it.
 struct SmpRow {
-  SmpShared* sh;
   const float* x;        // this CTA's slice
   int len, padded, begin;   // its length, that rounded up to whole warp loads, its first id
   bool wide;             // its 16-byte loads are aligned
@@ -187,6 +190,29 @@ __device__ __forceinline__ float4 smp_load4(const SmpRow& r, int i) {
   return v;
 }
 
+// f(x, i) for tokens x[0..3] = i .. i+3 of the slice, all of it (-inf in its
+// padding), four loads in flight a thread.  f works on four tokens at a time so
+// that their chains of 64-bit operations overlap: at 40 cycles an operation and
+// eight warps an SM's quarter they bound a pass otherwise.
+template <class F>
+__device__ __forceinline__ void smp_each(const SmpRow& r, F f) {
+  for (int i0 = threadIdx.x * 4; i0 < r.padded; i0 += kSmpThreads * 16) {
+    float4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + q * kSmpThreads * 4;
+      if (i < r.padded) v[q] = smp_load4(r, i);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + q * kSmpThreads * 4;
+      if (i >= r.padded) break;
+      const float x[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+      f(x, i);
+    }
+  }
+}
+
 // An integer W plus kSmpBias, the bits of 2^52: sums of these wrap, and the
 // bias is taken out of a sum at its end.
 constexpr u64 kSmpBias = 0x4330000000000000ull;
@@ -204,7 +230,7 @@ __device__ __forceinline__ u64 smp_bits(const SmpRow& r, float x) {
   double p = __fma_rn(f, a * a * a / 6.0, a * a / 2.0);
   p = __fma_rn(p, f, a);
   p = __fma_rn(p, f, 1.0);
-  p *= r.sh->tab[n & (kSmpTab - 1)];
+  p *= smp_shared()->tab[n & (kSmpTab - 1)];
   // times 2^((n >> 9) + 44) (a normal number: n >> 9 >= -61), then the integer nearest
   const double v = __hiloint2double(__double2hiint(p) + (((n >> 9) + kSmpOneBits) << 20),
                                     __double2loint(p));
@@ -228,7 +254,8 @@ __device__ __forceinline__ u64 smp_weight(const SmpRow& r, float x) {
 }
 
 // Block-wide sum; every thread gets it.
-__device__ __forceinline__ u64 smp_block_sum(SmpShared* sh, u64 v) {
+__device__ __forceinline__ u64 smp_block_sum(u64 v) {
+  SmpShared* sh = smp_shared();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   v = warp_sum_u64(v);
   __syncthreads();
@@ -240,7 +267,8 @@ __device__ __forceinline__ u64 smp_block_sum(SmpShared* sh, u64 v) {
   return v;
 }
 // Block-wide inclusive scan of one value a thread (in thread order).
-__device__ __forceinline__ u64 smp_block_scan(SmpShared* sh, u64 v) {
+__device__ __forceinline__ u64 smp_block_scan(u64 v) {
+  SmpShared* sh = smp_shared();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   v = warp_scan_u64(v, lane);
   __syncthreads();
@@ -252,8 +280,9 @@ __device__ __forceinline__ u64 smp_block_scan(SmpShared* sh, u64 v) {
   return v;
 }
 
-// Falling bitonic sort of a[0..n), n <= kSmpList.
-__device__ __noinline__ void smp_sort(u64* a, int n) {
+// Falling bitonic sort of list[0..n), n <= kSmpList.
+__device__ __noinline__ void smp_sort(int n) {
+  u64* a = smp_shared()->list;
   const int tid = threadIdx.x;
   int n2 = 64;
   while (n2 < n) n2 <<= 1;
@@ -281,11 +310,13 @@ __device__ __forceinline__ unsigned smp_bin(float m, float scale, float x) {
 
 // One candidate into this CTA's own list / that list into rank 0's, counted in
 // n_list[which] (past its room nothing is stored, only counted).
-__device__ __forceinline__ void smp_candidate(SmpShared* sh, float x, int id) {
+__device__ __forceinline__ void smp_candidate(float x, int id) {
+  SmpShared* sh = smp_shared();
   const unsigned at = atomicAdd(&sh->n_own, 1u);
   if (at < kSmpList) sh->own[at] = smp_key(smp_norm(x), id);
 }
-__device__ __forceinline__ void smp_hand_over(SmpShared* sh, int which) {
+__device__ __forceinline__ void smp_hand_over(int which) {
+  SmpShared* sh = smp_shared();
   __syncthreads();
   const unsigned n = sh->n_own;
   if (threadIdx.x == 0 && n) sh->own_at = add_peer_u32(&sh->n_list[which], 0, n);
@@ -296,7 +327,8 @@ __device__ __forceinline__ void smp_hand_over(SmpShared* sh, int which) {
     st_peer_u64(&sh->list[at + i], 0, sh->own[i]);
 }
 
-__device__ __forceinline__ void smp_clear(SmpShared* sh, int bins, bool by_mass) {
+__device__ __forceinline__ void smp_clear(int bins, bool by_mass) {
+  SmpShared* sh = smp_shared();
   for (int i = threadIdx.x; i < bins; i += kSmpThreads) {
     sh->cnt[i] = 0;
     if (by_mass) {
@@ -306,7 +338,8 @@ __device__ __forceinline__ void smp_clear(SmpShared* sh, int bins, bool by_mass)
   }
   __syncthreads();
 }
-__device__ __forceinline__ void smp_count(SmpShared* sh, unsigned b, bool by_mass, u64 w) {
+__device__ __forceinline__ void smp_count(unsigned b, bool by_mass, u64 w) {
+  SmpShared* sh = smp_shared();
   if (by_mass) {
     const unsigned lo = static_cast<unsigned>(w);
     const unsigned old = atomicAdd(&sh->mass[0][b], lo);
@@ -316,10 +349,35 @@ __device__ __forceinline__ void smp_count(SmpShared* sh, unsigned b, bool by_mas
   atomicAdd(&sh->cnt[b], 1u);
 }
 
+// Sums over the ranks of four neighbouring bins, all loads in flight at once:
+// f32(e, sum) and f64(e, sum) get bin e's, which fits either.
+template <class F32, class F64>
+__device__ __forceinline__ void smp_bins_of_all(const unsigned* bins, int ranks, F32 f32,
+                                                F64 f64) {
+  uint4 n[kSmpMaxCluster];
+#pragma unroll
+  for (int k = 0; k < kSmpMaxCluster; ++k)
+    n[k] = k < ranks ? ld_peer_v4(bins, k) : make_uint4(0, 0, 0, 0);
+  u64 t[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < kSmpMaxCluster; ++k) {
+    t[0] += n[k].x;
+    t[1] += n[k].y;
+    t[2] += n[k].z;
+    t[3] += n[k].w;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f32(e, static_cast<unsigned>(t[e]));
+    f64(e, t[e]);
+  }
+}
+
 struct SmpHit {
   unsigned bin;      // in the histogram
   u64 base, cnt;     // the measure before it, its tokens
   u64 all;           // the measure of all bins
+  u64 upto;          // tokens before and in it
 };
 // Rank 0: the last bin that holds anything and starts before the goal - the one in
 // which it is reached, or, if rounding lets none reach it, the last of all.
@@ -328,7 +386,7 @@ struct SmpHit {
 template <int BINS>
 __device__ SmpHit smp_merge(const SmpRow& r, bool by_mass, bool falling, u64 base, double top_p,
                             double& goal) {
-  SmpShared* sh = r.sh;
+  SmpShared* sh = smp_shared();
   const int tid = threadIdx.x;
   constexpr int kPer = BINS / kSmpThreads;   // bins of a thread, a multiple of four
   u64 v[kPer];
@@ -336,33 +394,24 @@ __device__ SmpHit smp_merge(const SmpRow& r, bool by_mass, bool falling, u64 bas
 #pragma unroll
   for (int q = 0; q < kPer; q += 4) {
     const int b = (falling ? BINS - kPer - tid * kPer : tid * kPer) + q;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[q + e] = 0;
-      c[q + e] = 0;
-    }
-    for (int k = 0; k < r.ranks; ++k) {
-      const uint4 n = ld_peer_v4(&sh->cnt[b], k);
-      c[q] += n.x;
-      c[q + 1] += n.y;
-      c[q + 2] += n.z;
-      c[q + 3] += n.w;
-      if (by_mass) {
-        const uint4 lo = ld_peer_v4(&sh->mass[0][b], k), hi = ld_peer_v4(&sh->mass[1][b], k);
-        v[q] += (static_cast<u64>(hi.x) << 32) + lo.x;
-        v[q + 1] += (static_cast<u64>(hi.y) << 32) + lo.y;
-        v[q + 2] += (static_cast<u64>(hi.z) << 32) + lo.z;
-        v[q + 3] += (static_cast<u64>(hi.w) << 32) + lo.w;
-      }
+    smp_bins_of_all(&sh->cnt[b], r.ranks, [&](int e, unsigned n) {
+      c[q + e] = n;
+    }, [&](int e, u64 n) { v[q + e] = n; });
+    if (by_mass) {
+      smp_bins_of_all(&sh->mass[0][b], r.ranks, [&](int, unsigned) {},
+                      [&](int e, u64 n) { v[q + e] = n; });
+      smp_bins_of_all(&sh->mass[1][b], r.ranks, [&](int, unsigned) {},
+                      [&](int e, u64 n) { v[q + e] += n << 32; });
     }
   }
   u64 sum = 0;
 #pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    if (!by_mass) v[q] = c[q];
-    sum += v[q];
-  }
-  u64 run = smp_block_scan(sh, sum);
+  for (int q = 0; q < kPer; ++q) sum += v[q];
+  u64 run = smp_block_scan(sum);
+  u64 tokens = 0;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) tokens += c[q];
+  tokens = smp_block_scan(tokens) - tokens;
   if (tid == kSmpThreads - 1) sh->bcast[0] = run;
   if (tid == 0) sh->bcast[1] = 0;
   __syncthreads();
@@ -371,14 +420,16 @@ __device__ SmpHit smp_merge(const SmpRow& r, bool by_mass, bool falling, u64 bas
   if (top_p >= 0.0) goal = fmax(top_p * static_cast<double>(h.all), 1.0);   // the first is kept
   run += base - sum;
   int hit = -1;
-  u64 hit_base = 0, hit_cnt = 0;
+  u64 hit_base = 0, hit_cnt = 0, hit_upto = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int q = falling ? kPer - 1 - j : j;
+    tokens += c[q];
     if (c[q] && static_cast<double>(run) < goal) {
       hit = (falling ? BINS - kPer - tid * kPer : tid * kPer) + q;
       hit_base = run;
       hit_cnt = c[q];
+      hit_upto = tokens;
     }
     run += v[q];
   }
@@ -389,16 +440,18 @@ __device__ SmpHit smp_merge(const SmpRow& r, bool by_mass, bool falling, u64 bas
   if (static_cast<int>(best >> 32) == tid + 1) {
     sh->bcast[2] = hit_base;
     sh->bcast[3] = hit_cnt;
+    sh->bcast[4] = hit_upto;
   }
   __syncthreads();
   h.bin = static_cast<unsigned>(best);
   h.base = sh->bcast[2];
   h.cnt = sh->bcast[3];
+  h.upto = sh->bcast[4];
   return h;
 }
 // Rank 0 tells every CTA; read as sh->told behind the next cluster barrier.
 __device__ __forceinline__ void smp_tell(const SmpRow& r, u64 v) {
-  if (threadIdx.x < r.ranks) st_peer_u64(&r.sh->told, threadIdx.x, v);
+  if (threadIdx.x < r.ranks) st_peer_u64(&smp_shared()->told, threadIdx.x, v);
 }
 
 // The border of a kept prefix among the tokens with key >= floor_key: the key
@@ -409,9 +462,9 @@ __device__ __forceinline__ void smp_tell(const SmpRow& r, u64 v) {
 //
 // Three radix levels find the value, then the ties at it are counted in
 // vocabulary order: right for any values, slow where many share a bin.
-__device__ __noinline__ u64 smp_border_radix(const SmpRow& r, bool by_mass, u64 floor_key,
+__device__ __noinline__ u64 smp_border_radix(const SmpRow r, bool by_mass, u64 floor_key,
                                              u64 want, double top_p, int which) {
-  SmpShared* sh = r.sh;
+  SmpShared* sh = smp_shared();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t prefix = 0;
   u64 base = 0;             // rank 0: tokens, or weight, above the current prefix
@@ -420,22 +473,20 @@ __device__ __noinline__ u64 smp_border_radix(const SmpRow& r, bool by_mass, u64 
   for (int level = 0; level < 3; ++level) {
     const int bits = level == 2 ? 10 : 11;
     const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
-    smp_clear(sh, kSmpRadix, by_mass);
-    for (int i0 = tid * 4; i0 < r.padded; i0 += kSmpThreads * 4) {
-      const float4 x4 = smp_load4(r, i0);
-      const float xs[4] = {x4.x, x4.y, x4.z, x4.w};
+    smp_clear(kSmpRadix, by_mass);
+    smp_each(r, [&](const float (&raw)[4], int i) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float x = smp_norm(xs[q]);
-        const u64 key = smp_key(x, r.begin + i0 + q);
+        const float x = smp_norm(raw[q]);
+        const u64 key = smp_key(x, r.begin + i + q);
         const uint32_t o = static_cast<uint32_t>(key >> 32);
-        if (i0 + q >= r.len || key < floor_key || (level > 0 && (o >> (shift + bits)) != prefix))
+        if (i + q >= r.len || key < floor_key || (level > 0 && (o >> (shift + bits)) != prefix))
           continue;
         u64 w = 0;
         if (by_mass && (w = smp_weight(r, x)) == 0) continue;
-        smp_count(sh, (o >> shift) & ((1u << bits) - 1), by_mass, w);
+        smp_count((o >> shift) & ((1u << bits) - 1), by_mass, w);
       }
-    }
+    });
     cluster_sync();
     if (r.rank == 0) {
       const SmpHit h = smp_merge<kSmpRadix>(r, by_mass, true, base,
@@ -473,7 +524,7 @@ __device__ __noinline__ u64 smp_border_radix(const SmpRow& r, bool by_mass, u64 
     mine += key >= tie_lo && key <= tie_hi;
   }
   const u64 in_warp = warp_sum_u64(mine);
-  const u64 upto = smp_block_scan(sh, lane == 0 ? in_warp : 0ull);
+  const u64 upto = smp_block_scan(lane == 0 ? in_warp : 0ull);
   const u64 warp_end = __shfl_sync(0xffffffffu, upto, 0);
   if (tid == kSmpThreads - 1)
     for (int k = 0; k < r.ranks; ++k) st_peer_u64(&sh->ties_in[which][r.rank], k, upto);
@@ -497,80 +548,24 @@ __device__ __noinline__ u64 smp_border_radix(const SmpRow& r, bool by_mass, u64 
   return sh->border[which];
 }
 
-// The same by histograms of linear bins: of what lies below the maximum, then
-// of the bin in which the border lies if it holds more than a list; the tokens
-// of the last bin are gathered and sorted.  Falls back to the radix search where
-// even that holds too many (ties).
-__device__ __noinline__ u64 smp_border(const SmpRow& r, float scale, bool by_mass, u64 floor_key,
-                                       u64 want, double top_p, int which) {
-  SmpShared* sh = r.sh;
+// Tokens of one bin of a histogram into rank 0's list, and of them the border:
+// the first at which `base` and their running measure reach the goal (base and
+// goal are rank 0's).
+template <class BinAt>
+__device__ __forceinline__ u64 smp_border_in_bin(const SmpRow& r, BinAt bin_at, unsigned bin,
+                                                 bool by_mass, u64 base, double goal, int which) {
+  SmpShared* sh = smp_shared();
   const int tid = threadIdx.x;
-  if (!r.fast) return smp_border_radix(r, by_mass, floor_key, want, top_p, which);
-  const float tau = floor_key ? smp_key_value(floor_key) : -INFINITY;
-  const int last = floor_key ? static_cast<int>(smp_id(floor_key)) - r.begin : 0x7fffffff;
-  unsigned bin = 0;
-  float shift = 0.f;         // second level: (m - x) scale - shift spans [0, 1]
-  u64 base = 0;              // rank 0
-  double goal = static_cast<double>(want);
-  // bin of x at a level; kSmpBins or more: not looked at
-  auto bin_at = [&](int level, float x, int i) -> unsigned {
-    unsigned b = smp_bin(r.m, scale, x);
-    if (level) {
-      if (b != bin) return kSmpBins;
-      const float f = fmaxf(fmaf(r.m - x, scale, -shift), 0.f);
-      b = min(__float_as_uint(fmaf(f, kSmpBins - 2.f, 8388608.f)) - 0x4B000000u,
-              kSmpBins - 1u);
-    }
-    return x > tau || (x == tau && i <= last) ? b : kSmpBins;
-  };
-  unsigned sub = 0;
-  int level = 0;
-  constexpr u64 kRefine = 1ull << 32, kNothing = 2ull << 32;
-  for (;; ++level) {
-    smp_clear(sh, kSmpBins, by_mass);
-    for (int i0 = tid * 4; i0 < r.padded; i0 += kSmpThreads * 4) {
-      const float4 x4 = smp_load4(r, i0);
-      const float xs[4] = {x4.x, x4.y, x4.z, x4.w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const unsigned b = bin_at(level, xs[q], i0 + q);
-        if (b >= kSmpBins) continue;
-        u64 w = 0;
-        if (by_mass && (w = smp_weight(r, xs[q])) == 0) continue;
-        smp_count(sh, b, by_mass, w);
-      }
-    }
-    cluster_sync();
-    if (r.rank == 0) {
-      const SmpHit h = smp_merge<kSmpBins>(r, by_mass, false, base,
-                                           by_mass && level == 0 ? top_p : -1.0, goal);
-      base = h.base;
-      // fewer than wanted weigh anything: nothing to cut
-      const bool nothing = level == 0 && (h.all == 0 || (!by_mass && h.all < want));
-      smp_tell(r, nothing ? kNothing : h.cnt > kSmpList ? kRefine | h.bin : h.bin);
-    }
-    if (tid == 0) sh->n_own = 0;
-    cluster_sync();
-    const u64 told = sh->told;
-    sub = static_cast<unsigned>(told);
-    if (told >= kNothing) return floor_key;
-    if (told < kRefine) break;
-    if (level) return smp_border_radix(r, by_mass, floor_key, want, top_p, which);
-    bin = sub;
-    shift = static_cast<float>(sub) - 0.5f;
-  }
-  for (int i0 = tid * 4; i0 < r.padded; i0 += kSmpThreads * 4) {
-    const float4 x4 = smp_load4(r, i0);
-    const float xs[4] = {x4.x, x4.y, x4.z, x4.w};
+  smp_each(r, [&](const float (&x)[4], int i) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (bin_at(level, xs[q], i0 + q) == sub) smp_candidate(sh, xs[q], r.begin + i0 + q);
-  }
-  smp_hand_over(sh, 1 + which);
+      if (bin_at(x[q], i + q) == bin) smp_candidate(x[q], r.begin + i + q);
+  });
+  smp_hand_over(1 + which);
   cluster_sync();
   if (r.rank == 0) {
     const int n = min(sh->n_list[1 + which], static_cast<unsigned>(kSmpList));
-    smp_sort(sh->list, n);
+    smp_sort(n);
     constexpr int kPer = kSmpList / kSmpThreads;
     const int i0 = kPer * tid;
     u64 w[kPer], sum = 0;
@@ -579,7 +574,7 @@ __device__ __noinline__ u64 smp_border(const SmpRow& r, float scale, bool by_mas
       w[q] = i0 + q < n ? (by_mass ? smp_weight(r, smp_key_value(sh->list[i0 + q])) : 1ull) : 0ull;
       sum += w[q];
     }
-    u64 at = base + smp_block_scan(sh, sum) - sum;
+    u64 at = base + smp_block_scan(sum) - sum;
     if (tid == 0) sh->first_bad = 0;
     __syncthreads();
 #pragma unroll
@@ -592,6 +587,137 @@ __device__ __noinline__ u64 smp_border(const SmpRow& r, float scale, bool by_mas
   }
   cluster_sync();
   return sh->border[which];
+}
+
+// What rank 0 tells besides a bin.
+constexpr u64 kSmpRefine = 1ull << 32, kSmpNothing = 2ull << 32;
+
+// The border of top_k = want: a histogram of linear bins below the maximum, of
+// the bin in which the border lies if that holds more than a list, and the
+// sorted list.  The radix search where even that holds more (ties).
+__device__ __noinline__ u64 smp_border_k(const SmpRow r, float scale, u64 want) {
+  SmpShared* sh = smp_shared();
+  if (!r.fast) return smp_border_radix(r, false, 0ull, want, 0.0, 0);
+  unsigned bin = 0;
+  float shift = 0.f;         // second level: (m - x) scale - shift spans [0, 1]
+  u64 base = 0;              // rank 0
+  double goal = static_cast<double>(want);
+  int level = 0;
+  // kSmpBins or more: not looked at
+  auto bin_at = [&](float x, int) -> unsigned {
+    const unsigned b = smp_bin(r.m, scale, x);
+    if (level == 0) return b;
+    if (b != bin) return kSmpBins;
+    const float f = fmaxf(fmaf(r.m - x, scale, -shift), 0.f);
+    return min(__float_as_uint(fmaf(f, kSmpBins - 2.f, 8388608.f)) - 0x4B000000u, kSmpBins - 1u);
+  };
+  for (;; ++level) {
+    smp_clear(kSmpBins, false);
+    smp_each(r, [&](const float (&x)[4], int i) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const unsigned b = bin_at(x[q], i + q);
+        if (b < kSmpBins) atomicAdd(&sh->cnt[b], 1u);
+      }
+    });
+    cluster_sync();
+    if (r.rank == 0) {
+      const SmpHit h = smp_merge<kSmpBins>(r, false, false, base, -1.0, goal);
+      base = h.base;
+      // fewer than wanted weigh anything: nothing to cut
+      smp_tell(r, level == 0 && h.all < want ? kSmpNothing
+                  : h.cnt > kSmpList         ? kSmpRefine | h.bin
+                                             : h.bin);
+    }
+    if (threadIdx.x == 0) sh->n_own = 0;
+    cluster_sync();
+    const u64 told = sh->told;
+    if (told >= kSmpNothing) return 0ull;
+    if (told < kSmpRefine)
+      return smp_border_in_bin(r, bin_at, static_cast<unsigned>(told), false, base, goal, 0);
+    if (level) return smp_border_radix(r, false, 0ull, want, 0.0, 0);
+    bin = static_cast<unsigned>(told);
+    shift = static_cast<float>(bin) - 0.5f;
+  }
+}
+
+// top_p over the tokens with key >= floor_key: a histogram of their weights in
+// linear bins, of the bin in which the border lies if that holds more than a
+// list, and the sorted list.  Sums of integers are exact, so the bins say exactly
+// where the border lies.  If a list can hold all tokens up to it, the list is
+// filled (`listed` is set, rank 0 has the weight of all in mass_all) and the
+// caller draws from it.  The radix search where even the second histogram leaves
+// too many (ties).
+__device__ __noinline__ u64 smp_border_p(const SmpRow r, float scale, u64 floor_key,
+                                         double top_p, bool* listed, u64* mass_all) {
+  SmpShared* sh = smp_shared();
+  const int tid = threadIdx.x;
+  *listed = false;
+  if (!r.fast) return smp_border_radix(r, true, floor_key, 0ull, top_p, 1);
+  const float tau = floor_key ? smp_key_value(floor_key) : -INFINITY;
+  const int last = floor_key ? static_cast<int>(smp_id(floor_key)) - r.begin : 0x7fffffff;
+  const bool plain = floor_key == 0 && r.w_min == 0;
+  auto kept = [&](float x, int i) { return x > tau || (x == tau && i <= last); };
+  scale *= static_cast<float>(kSmpRadix / kSmpBins);    // finer bins: a weight costs more
+  unsigned bin = 0;
+  float shift = 0.f;         // second level: (m - x) scale - shift spans [0, 1]
+  int level = 0;
+  // kSmpRadix or more: not looked at
+  auto bin_at = [&](float x, int i) -> unsigned {
+    const unsigned b = smp_bin(r.m, scale, x);
+    if (!plain && !kept(x, i)) return kSmpRadix;
+    if (level == 0) return b;
+    if (b != bin) return kSmpRadix;
+    const float f = fmaxf(fmaf(r.m - x, scale, -shift), 0.f);
+    return min(__float_as_uint(fmaf(f, kSmpRadix - 2.f, 8388608.f)) - 0x4B000000u,
+               kSmpRadix - 1u);
+  };
+  u64 base = 0;              // rank 0
+  double goal = 0.0;
+  for (;; ++level) {
+    smp_clear(kSmpRadix, true);
+    smp_each(r, [&](const float (&x)[4], int i) {
+      unsigned b[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) b[q] = bin_at(x[q], i + q);
+      if (min(min(b[0], b[1]), min(b[2], b[3])) >= kSmpRadix) return;
+      u64 w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[q] = smp_bits(r, x[q]) - kSmpBias;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (b[q] < kSmpRadix && w[q] && w[q] >= r.w_min) smp_count(b[q], true, w[q]);
+    });
+    cluster_sync();
+    if (r.rank == 0) {
+      const SmpHit h = smp_merge<kSmpRadix>(r, true, false, base, level == 0 ? top_p : -1.0, goal);
+      base = h.base;
+      if (level == 0) *mass_all = h.all;
+      smp_tell(r, level == 0 && h.upto <= kSmpList ? kSmpNothing | h.bin
+                  : h.cnt > kSmpList               ? kSmpRefine | h.bin
+                                                   : h.bin);
+    }
+    if (tid == 0) sh->n_own = 0;
+    cluster_sync();
+    const u64 told = sh->told;
+    bin = level == 0 ? static_cast<unsigned>(told) : bin;
+    if (told >= kSmpNothing) break;
+    if (told < kSmpRefine)
+      return smp_border_in_bin(r, bin_at, static_cast<unsigned>(told), true, base, goal, 1);
+    if (level) return smp_border_radix(r, true, floor_key, 0ull, top_p, 1);
+    shift = static_cast<float>(bin) - 0.5f;
+  }
+  smp_each(r, [&](const float (&x)[4], int i) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (bin_at(x[q], i + q) <= bin) smp_candidate(x[q], r.begin + i + q);
+  });
+  smp_hand_over(3);
+  cluster_sync();
+  // tokens of these bins that min_p filters are in the list too
+  *listed = ld_peer_u32(&sh->n_list[3], 0) <= kSmpList;
+  cluster_sync();
+  return *listed ? floor_key : smp_border_radix(r, true, floor_key, 0ull, top_p, 1);
 }
 
 struct SmpResult {
@@ -617,27 +743,41 @@ __device__ __forceinline__ float smp_share(u64 w, u64 total) {
 // the row.  draft >= 0: first offered for acceptance with u_accept.
 __device__ __forceinline__ SmpResult smp_draw_row(const SmpRow& r, u64 floor_key, int draft,
                                                   float u_accept, float u) {
-  SmpShared* sh = r.sh;
+  SmpShared* sh = smp_shared();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float tau = floor_key ? smp_key_value(floor_key) : -INFINITY;
   const int last = floor_key ? static_cast<int>(smp_id(floor_key)) - r.begin : 0x7fffffff;
   // kept: above the border's value, or at it and not behind its id
-  auto weight = [&](float x, int i) -> u64 {
-    return x > tau || (x == tau && i <= last) ? smp_weight(r, x) : 0ull;
-  };
+  auto keep = [&](float x, int i) { return x > tau || (x == tau && i <= last); };
+  auto weight = [&](float x, int i) -> u64 { return keep(x, i) ? smp_weight(r, x) : 0ull; };
   // warps own runs of 128-token groups, a lane four neighbours of a group
   const int seg = ((r.padded >> 7) + kSmpWarps - 1) / kSmpWarps * 128;
   const int beg = min(r.padded, warp * seg), end = min(r.padded, beg + seg);
   const int draft_at = draft - r.begin;
   u64 mine = 0;
-  if (floor_key == 0 && r.fast && r.w_min == 0) {
-#pragma unroll 2
-    for (int i = beg + lane * 4; i < end; i += 128) {
-      const float4 v = smp_load4(r, i);
-      mine += smp_bits(r, v.x) + smp_bits(r, v.y);
-      mine += smp_bits(r, v.z) + smp_bits(r, v.w);
+  if (r.fast && r.w_min == 0) {
+    for (int i0 = beg + lane * 4; i0 < end; i0 += 512) {
+      float4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (i0 + q * 128 < end) v[q] = smp_load4(r, i0 + q * 128);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + q * 128;
+        if (i >= end) break;
+        const u64 a = smp_bits(r, v[q].x), b = smp_bits(r, v[q].y), c = smp_bits(r, v[q].z),
+                  d = smp_bits(r, v[q].w);
+        if (floor_key == 0) {
+          mine += a + b;
+          mine += c + d;
+          mine -= 4 * kSmpBias;
+        } else {
+          mine += (keep(v[q].x, i) ? a - kSmpBias : 0) + (keep(v[q].y, i + 1) ? b - kSmpBias : 0);
+          mine += (keep(v[q].z, i + 2) ? c - kSmpBias : 0) +
+                  (keep(v[q].w, i + 3) ? d - kSmpBias : 0);
+        }
+      }
     }
-    mine -= static_cast<u64>((end - beg) / 32) * kSmpBias;
   } else {
     for (int i = beg + lane * 4; i < end; i += 128) {
       const float4 v = smp_load4(r, i);
@@ -645,7 +785,7 @@ __device__ __forceinline__ SmpResult smp_draw_row(const SmpRow& r, u64 floor_key
     }
   }
   const u64 in_warp = warp_sum_u64(mine);
-  const u64 upto = smp_block_scan(sh, lane == 0 ? in_warp : 0ull);
+  const u64 upto = smp_block_scan(lane == 0 ? in_warp : 0ull);
   if (tid == kSmpThreads - 1) {
     const u64 d = draft >= 0 && draft_at >= 0 && draft_at < r.len
                       ? weight(__ldg(r.x + draft_at), draft_at)
@@ -715,7 +855,7 @@ __device__ __forceinline__ SmpResult smp_draw_row(const SmpRow& r, u64 floor_key
                  : weight(x[q], i + q);
       sum += w[q];
     }
-    u64 at = run + smp_block_scan(sh, sum);
+    u64 at = run + smp_block_scan(sum);
     if (tid == kSmpThreads - 1) sh->bcast[1] = at;
     at -= sum;
 #pragma unroll
@@ -741,7 +881,7 @@ __device__ __forceinline__ SmpResult smp_draw_few(const SmpRow& r, int n, int k,
                                                   float u) {
   // n <= kSmpFew: kShare threads compare a candidate with all others, so its
   // place, and the weight before it in either order, need no sort
-  SmpShared* sh = r.sh;
+  SmpShared* sh = smp_shared();
   const int tid = threadIdx.x;
   constexpr int kShare = kSmpThreads / kSmpFew;
   const int i = tid / kShare, q0 = tid % kShare;
@@ -804,13 +944,13 @@ __device__ __forceinline__ SmpResult smp_draw_few(const SmpRow& r, int n, int k,
   }
   return out;
 }
-__device__ __noinline__ SmpResult smp_draw_list(const SmpRow& r, int n, int k, double top_p,
+__device__ __noinline__ SmpResult smp_draw_list(const SmpRow r, int n, int k, double top_p,
                                                 u64 mass_all, int draft, float u_accept, float u) {
-  SmpShared* sh = r.sh;
+  SmpShared* sh = smp_shared();
   const int tid = threadIdx.x;
   constexpr int kPer = kSmpList / kSmpThreads;
   SmpResult out = {0, 0, -1, 0.f};
-  smp_sort(sh->list, n);
+  smp_sort(n);
   if (tid == 0) {
     sh->first_bad = n;
     sh->bcast[2] = 0;
@@ -824,7 +964,7 @@ __device__ __noinline__ SmpResult smp_draw_list(const SmpRow& r, int n, int k, d
     w[q] = i < n && (k <= 0 || i < k) ? smp_weight(r, smp_key_value(sh->list[i])) : 0ull;
     sum += w[q];
   }
-  u64 run = smp_block_scan(sh, sum);
+  u64 run = smp_block_scan(sum);
   if (tid == kSmpThreads - 1) sh->bcast[0] = run;
   __syncthreads();
   run -= sum;
@@ -854,7 +994,7 @@ __device__ __noinline__ SmpResult smp_draw_list(const SmpRow& r, int n, int k, d
 #pragma unroll
   for (int q = 0; q < kPer; ++q)
     if (i0 + q < n) sh->list[i0 + q] = key[q];
-  smp_sort(sh->list, n);
+  smp_sort(n);
   const u64 draft_w = sh->bcast[2];
   int id[kPer];
   sum = 0;
@@ -867,7 +1007,7 @@ __device__ __noinline__ SmpResult smp_draw_list(const SmpRow& r, int n, int k, d
     if (id[q] == draft) w[q] = 0;
     sum += w[q];
   }
-  run = smp_block_scan(sh, sum);
+  run = smp_block_scan(sum);
   if (tid == kSmpThreads - 1) sh->bcast[1] = run;
   __syncthreads();
   const u64 total = sh->bcast[1];             // without the draft
@@ -897,12 +1037,12 @@ __device__ __noinline__ SmpResult smp_draw_list(const SmpRow& r, int n, int k, d
 
 // One row: maxima, filters, draw.  Exactly one thread of the cluster returns with
 // writer set.
-__device__ __forceinline__ SmpResult smp_row(SmpShared* sh, const float* row, int V, int slice,
+__device__ __forceinline__ SmpResult smp_row(const float* row, int V, int slice,
                                              const SampleSettings& set, int at, int draft,
                                              float u_accept, float u) {
+  SmpShared* sh = smp_shared();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   SmpRow r;
-  r.sh = sh;
   r.rank = static_cast<int>(cluster_rank());
   r.ranks = gridDim.x;
   r.begin = r.rank * slice;
@@ -933,13 +1073,13 @@ __device__ __forceinline__ SmpResult smp_row(SmpShared* sh, const float* row, in
   const bool by_p = p_in < 1.f;
   const double top_p = p_in > 0.f ? static_cast<double>(p_in) : 0.0;
   const float scale = fminf((kSmpBins - 1) / (kSmpReach * T), 3e38f);
-  const bool by_list = !greedy && (by_k ? k_in <= kSmpListTopK : by_p);
+  const bool by_list = !greedy && by_k && k_in <= kSmpListTopK;
   if (!greedy) {
     for (int i = tid; i < kSmpTab; i += kSmpThreads) sh->tab[i] = exp2(i * (1.0 / kSmpTab));
     if (by_list)
       for (int i = tid; i < kSmpBins; i += kSmpThreads) sh->cnt[i] = 0;
   }
-  if (tid < 3) sh->n_list[tid] = 0;
+  if (tid < 4) sh->n_list[tid] = 0;
   if (tid < 4) sh->thr[tid] = -INFINITY;
   if (tid == 0) {
     sh->n_own = 0;
@@ -979,7 +1119,7 @@ __device__ __forceinline__ SmpResult smp_row(SmpShared* sh, const float* row, in
     for (int w = 0; w < kSmpWarps; ++w)
       if (w < warp) run += warp_u[w];
     run -= sum;
-    const unsigned aim = by_k ? static_cast<unsigned>(k_in) : static_cast<unsigned>(kSmpAim);
+    const unsigned aim = static_cast<unsigned>(k_in);
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
 #pragma unroll
@@ -1054,79 +1194,39 @@ __device__ __forceinline__ SmpResult smp_row(SmpShared* sh, const float* row, in
   const double below = (r.md - static_cast<double>(r.x_cut)) * r.c;
   r.fast = r.x_cut > -INFINITY && r.m < INFINITY && below >= 46.0 * kSmpTab &&
            below <= 60.0 * kSmpTab;
+  u64 floor_key = 0, mass_all = 0;
+  bool listed = false;
   if (by_list && r.fast) {
-    // tokens further down than x_cut weigh nothing
-    const bool whole = !(cut > r.x_cut);
-    cut = fmaxf(cut, r.x_cut);
-    u64 mass = 0;
-    if (by_k) {
-      if (mine >= cut)
-        for (int i = tid * 4; i < r.padded; i += kSmpThreads * 4) {
-          const float4 v = smp_load4(r, i);
-          if (v.x >= cut) smp_candidate(sh, v.x, r.begin + i);
-          if (v.y >= cut) smp_candidate(sh, v.y, r.begin + i + 1);
-          if (v.z >= cut) smp_candidate(sh, v.z, r.begin + i + 2);
-          if (v.w >= cut) smp_candidate(sh, v.w, r.begin + i + 3);
-        }
-    } else {                 // top_p refers to the whole row's weight
-#pragma unroll 2
-      for (int i = tid * 4; i < r.padded; i += kSmpThreads * 4) {
+    cut = fmaxf(cut, r.x_cut);         // tokens further down weigh nothing
+    // a warp looks at the tokens of each of its threads that reached the cut
+    for (unsigned hot = __ballot_sync(0xffffffffu, mine >= cut); hot; hot &= hot - 1) {
+      const int of = (warp * 32 + __ffs(hot) - 1) * 4;
+      for (int i = of + lane * kSmpThreads * 4; i < r.padded; i += kSmpThreads * 128) {
         const float4 v = smp_load4(r, i);
-        if (fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= cut) {
-          if (v.x >= cut) smp_candidate(sh, v.x, r.begin + i);
-          if (v.y >= cut) smp_candidate(sh, v.y, r.begin + i + 1);
-          if (v.z >= cut) smp_candidate(sh, v.z, r.begin + i + 2);
-          if (v.w >= cut) smp_candidate(sh, v.w, r.begin + i + 3);
-        }
-        if (r.w_min) {
-          mass += smp_weight(r, v.x) + smp_weight(r, v.y) + smp_weight(r, v.z) +
-                  smp_weight(r, v.w);
-        } else {
-          mass += smp_bits(r, v.x) + smp_bits(r, v.y);
-          mass += smp_bits(r, v.z) + smp_bits(r, v.w);
-          mass -= 4 * kSmpBias;
-        }
+        if (v.x >= cut) smp_candidate(v.x, r.begin + i);
+        if (v.y >= cut) smp_candidate(v.y, r.begin + i + 1);
+        if (v.z >= cut) smp_candidate(v.z, r.begin + i + 2);
+        if (v.w >= cut) smp_candidate(v.w, r.begin + i + 3);
       }
-      mass = smp_block_sum(sh, mass);
-      if (tid == 0) st_peer_u64(&sh->mass_in[r.rank], 0, mass);
     }
-    smp_hand_over(sh, 0);
+    smp_hand_over(0);
     cluster_sync();
-    if (r.rank == 0) {
-      const int n = sh->n_list[0];
-      bool all_in = n <= kSmpList;
-      u64 mass_all = 0;
-      if (!by_k) {
-        for (int k = 0; k < r.ranks; ++k) mass_all += sh->mass_in[k];
-        if (all_in && !whole) {      // does the list reach top_p of the row's weight?
-          u64 w = 0;
-          for (int i = tid; i < n; i += kSmpThreads)
-            w += smp_weight(r, smp_key_value(sh->list[i]));
-          w = smp_block_sum(sh, w);
-          all_in = static_cast<double>(w) >= top_p * static_cast<double>(mass_all);
-        }
-      }
-      if (tid < r.ranks) st_peer_u32(&sh->verdict, tid, all_in);
-      cluster_sync();
-      if (all_in) {
-        const int k = by_k ? k_in : 0;
-        const double p = by_p ? top_p : 2.0;
-        return n <= kSmpFew ? smp_draw_few(r, n, k, p, mass_all, draft, u_accept, u)
-                            : smp_draw_list(r, n, k, p, mass_all, draft, u_accept, u);
-      }
-    } else {
-      cluster_sync();
-      if (sh->verdict) {
-        out.writer = 0;
-        return out;
-      }
-    }
+    if (r.rank == 0 && tid < r.ranks) st_peer_u32(&sh->verdict, tid, sh->n_list[0] <= kSmpList);
+    cluster_sync();
+    listed = sh->verdict != 0;
   }
-  // the whole row, from the exact borders where there are any
-  u64 floor_key = 0;
-  if (by_k) floor_key = smp_border(r, scale, false, 0ull, static_cast<u64>(k_in), 0.0, 0);
-  if (by_p) floor_key = smp_border(r, scale, true, floor_key, 0ull, top_p, 1);
-  return smp_draw_row(r, floor_key, draft, u_accept, u);
+  if (!listed) {
+    if (by_k) floor_key = smp_border_k(r, scale, static_cast<u64>(k_in));
+    if (by_p) floor_key = smp_border_p(r, scale, floor_key, top_p, &listed, &mass_all);
+  }
+  if (!listed) return smp_draw_row(r, floor_key, draft, u_accept, u);
+  out.writer = 0;
+  if (r.rank != 0) return out;
+  const bool by_border = mass_all != 0;      // listed by border_p: top_k is done
+  const int n = sh->n_list[by_border ? 3 : 0], k = by_k && !by_border ? k_in : 0;
+  const double p = by_p ? top_p : 2.0;
+  return n <= kSmpFew ? smp_draw_few(r, n, k, p, mass_all, draft, u_accept, u)
+                      : smp_draw_list(r, n, k, p, mass_all, draft, u_accept, u);
 }
 
 struct SampleParams {
@@ -1142,12 +1242,11 @@ struct SampleParams {
 
 // Cluster y draws row y's token.
 __global__ void __launch_bounds__(kSmpThreads, kSmpCtas) sample_kernel(const SampleParams p) {
-  __shared__ SmpShared shared;
   pdl_trigger();
   pdl_wait();
-  SmpShared* sh = &shared;
+  SmpShared* sh = smp_shared();
   const int row = blockIdx.y;
-  const SmpResult res = smp_row(sh, p.logits + static_cast<int64_t>(row) * p.ld, p.V, p.slice,
+  const SmpResult res = smp_row(p.logits + static_cast<int64_t>(row) * p.ld, p.V, p.slice,
                                 p.set, row, -1, 0.f, p.u[row]);
   if (res.writer) {
     p.tokens[row] = res.token;
@@ -1179,10 +1278,9 @@ struct VerifySampledParams {
 // last rows writes the answer.
 __global__ void __launch_bounds__(kSmpThreads, kSmpCtas)
 verify_sampled_kernel(const VerifySampledParams p) {
-  __shared__ SmpShared shared;
   pdl_trigger();
   pdl_wait();
-  SmpShared* sh = &shared;
+  SmpShared* sh = smp_shared();
   const int b = blockIdx.y, K = p.K;
   const int first = blockIdx.z * p.run, end = min(K + 1, first + p.run);
   const bool lead = threadIdx.x == 0 && cluster_rank() == 0;
@@ -1201,7 +1299,7 @@ verify_sampled_kernel(const VerifySampledParams p) {
   for (int i = first; needed && i < end; ++i) {
     const int draft = i < K ? p.drafts[static_cast<int64_t>(b) * K + i] : -1;
     const SmpResult res =
-        smp_row(sh, p.logits + (static_cast<int64_t>(b) * (K + 1) + i) * p.ld, p.V, p.slice, p.set,
+        smp_row(p.logits + (static_cast<int64_t>(b) * (K + 1) + i) * p.ld, p.V, p.slice, p.set,
                 b, draft, i < K ? p.u_accept[static_cast<int64_t>(b) * K + i] : 0.f,
                 p.u_sample[b]);
     if (res.writer && (!res.accepted || i == K)) {
