@@ -43,17 +43,8 @@ void launch_append(dflash_handle* h, const AppendParams& p, cudaStream_t st) {
   }
 }
 
-// Cluster size and slice for a vocabulary: a CTA a slice of up to 8192 tokens,
-// at most eight CTAs (the portable cluster size).
-struct SamplePlan {
-  int ranks = 1, slice = 0;
-};
-SamplePlan plan_sample(int V) {
-  SamplePlan p;
-  while (p.ranks < kSmpMaxCluster && p.ranks * 8192 < V) p.ranks *= 2;
-  p.slice = (cdiv(V, p.ranks) + 3) / 4 * 4;
-  return p;
-}
+// Tokens of a CTA's slice of a row.
+int sample_slice(int V) { return (cdiv(V, kSmpRanks) + 3) / 4 * 4; }
 
 // Attention over a shared prefix: which kernel takes the prefix, how it is
 // dealt, the splits of the requests' own keys, and the workspace.
@@ -296,19 +287,18 @@ dflash_status dflash_sample_tokens(const float* logits, int64_t ld, int rows, in
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dflash_status s = set_device_for(st, tokens);
   if (s != DFLASH_OK) return s;
-  const SamplePlan pl = plan_sample(V);
   SampleParams p;
   p.logits = logits;
   p.ld = ld;
   p.rows = rows;
   p.V = V;
-  p.slice = pl.slice;
+  p.slice = sample_slice(V);
   p.set = {temperature, top_k, top_p, min_p};
   p.u = u;
   p.tokens = tokens;
   p.probs = probs;
   p.err = device_error;
-  launch_kc(pdl_default(), pl.ranks, sample_kernel, dim3(pl.ranks, rows), dim3(kSmpThreads),
+  launch_kc(pdl_default(), kSmpRanks, sample_kernel, dim3(kSmpRanks, rows), dim3(kSmpThreads),
             sizeof(SmpShared), st, p);
   return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
@@ -336,7 +326,6 @@ dflash_status dflash_verify_sampled(const int32_t* drafts, const float* target_l
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dflash_status s = set_device_for(st, out_tokens);
   if (s != DFLASH_OK) return s;
-  const SamplePlan pl = plan_sample(V);
   VerifySampledParams p;
   p.drafts = drafts;
   p.logits = target_logits;
@@ -344,7 +333,7 @@ dflash_status dflash_verify_sampled(const int32_t* drafts, const float* target_l
   p.B = B;
   p.K = K;
   p.V = V;
-  p.slice = pl.slice;
+  p.slice = sample_slice(V);
   p.set = {temperature, top_k, top_p, min_p};
   p.u_accept = u_accept;
   p.u_sample = u_sample;
@@ -357,10 +346,7 @@ dflash_status dflash_verify_sampled(const int32_t* drafts, const float* target_l
   p.row_token = static_cast<int32_t*>(workspace) + 2 * static_cast<int64_t>(B);
   launch_k(pdl_default(), zero_words_kernel, dim3(std::min(cdiv(2 * B, 256), 64)), dim3(256), 0,
            st, p.done, 2 * B);
-  // Few rows all run at once; of many, a cluster takes a run of a request's rows,
-  // so that the ones behind a refused draft cost no launch.
-  p.run = std::max(1, std::min(8, B * (K + 1) / 96));
-  launch_kc(pdl_default(), pl.ranks, verify_sampled_kernel, dim3(pl.ranks, B, cdiv(K + 1, p.run)),
+  launch_kc(pdl_default(), kSmpRanks, verify_sampled_kernel, dim3(kSmpRanks, B, K + 1),
             dim3(kSmpThreads), sizeof(SmpShared), st, p);
   return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }

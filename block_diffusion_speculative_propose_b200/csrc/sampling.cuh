@@ -35,9 +35,9 @@ namespace dflash {
 constexpr int kSmpThreads = 256;
 constexpr int kSmpWarps = kSmpThreads / 32;
 constexpr int kSmpCtas = 4;           // of an SM
-constexpr int kSmpMaxCluster = 8;
-constexpr int kSmpBins = 1024;        // linear bins of x below the maximum
-constexpr int kSmpRadix = 2048;       // bins of a radix level (11 bits)
+constexpr int kSmpRanks = 8;          // CTAs of a row (the largest portable cluster)
+constexpr int kSmpBins = kSmpRanks * kSmpThreads;   // of a histogram: each thread merges one
+constexpr int kSmpMaxBins = 1024;     // bins of the threads' maxima
 constexpr int kSmpList = 1024;        // candidates that one CTA sorts
 constexpr int kSmpFew = 128;          // candidates that are ranked by comparing all pairs
 constexpr int kSmpListTopK = 640;     // largest top_k whose candidates are gathered by maxima
@@ -58,32 +58,34 @@ struct SampleSettings {
 // Every field that a peer writes or reads is used once a row, so a barrier
 // between the writing and the reading is all it needs.
 struct SmpShared {
-  double tab[kSmpTab];
+  double tab[kSmpTab];               // 2^(44 + j / 512)
   u64 warp_a[kSmpWarps];             // block-wide sums
-  u64 bcast[5];
-  u64 kept_in[kSmpMaxCluster];       // from each rank: its kept weight, the draft's
-  u64 draft_in[kSmpMaxCluster];
-  u64 ties_in[2][kSmpMaxCluster];    // from each rank: ties of the border value (two searches)
+  u64 bcast[4];
+  u64 all_in[2][kSmpRanks];          // from each rank: measure and tokens of its bins
+  u64 hit[4];                        // from the rank that has it: bin, base, tokens, tokens up to it
+  u64 kept_in[kSmpRanks];            // from each rank: its kept weight, the draft's
+  u64 draft_in[kSmpRanks];
+  u64 ties_in[2][kSmpRanks];         // from each rank: ties of the border value (two searches)
   u64 border[2];                     // the border key (two searches)
-  u64 told, n_keep;                  // from rank 0: how a search goes on
-  float top_in[kSmpMaxCluster];      // from each rank: the largest value of its slice
-  float thr_in[kSmpMaxCluster][4];   // and values that ever fewer of its tokens reach
+  float top_in[kSmpRanks];           // from each rank: the largest value of its slice
+  float thr_in[kSmpRanks][4];        // and values that ever fewer of its tokens reach
   float thr[4];
-  unsigned first_in[kSmpMaxCluster]; // greedy: the first id that holds the largest value
+  unsigned first_in[kSmpRanks];      // greedy: the first id that holds the largest value
   unsigned first;
   unsigned n_list[4];                // rank 0: candidates gathered (four lists)
   unsigned n_own, own_at;            // this CTA's share of them, its place
-  unsigned verdict, told32;          // from rank 0
-  unsigned first_bad;
+  unsigned verdict, more;            // from rank 0
+  unsigned found, n_bucket;
   union {
-    __align__(16) unsigned cnt[kSmpRadix];   // histogram: tokens
-    u64 own[kSmpList];                       // this CTA's candidates
+    unsigned cnt[kSmpBins];          // histogram: tokens
+    u64 own[kSmpList];               // this CTA's candidates
+    u64 bucket[kSmpList];            // rank 0: places in the list
   };
   union {
-    __align__(16) unsigned mass[2][kSmpRadix];   // histogram: low, high words of weights
+    unsigned mass[2][kSmpBins];      // histogram: low, high words of weights
     struct {
-      u64 list[kSmpList];                        // rank 0: the candidates' keys
-      u64 w[kSmpList];
+      u64 list[kSmpList];            // rank 0: the candidates' keys
+      u64 w[kSmpList];               // and their weights
     };
   };
 };
@@ -112,19 +114,6 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
-}
-__device__ __forceinline__ uint4 ld_peer_v4(const void* p, uint32_t rank) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(peer_addr(p, rank))
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ u64 ld_peer_u64(const void* p, uint32_t rank) {
-  u64 v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer_addr(p, rank)) : "memory");
-  return v;
 }
 __device__ __forceinline__ uint32_t ld_peer_u32(const void* p, uint32_t rank) {
   uint32_t v;
@@ -171,7 +160,7 @@ struct SmpRow {
   const float* x;        // this CTA's slice
   int len, padded, begin;   // its length, that rounded up to whole warp loads, its first id
   bool wide;             // its 16-byte loads are aligned
-  int rank, ranks;
+  int rank;
   float m;               // the row's largest value
   float x_cut;           // weighs nothing
   double md, c;          // m, 512 log2(e) / T
@@ -231,8 +220,8 @@ __device__ __forceinline__ u64 smp_bits(const SmpRow& r, float x) {
   p = __fma_rn(p, f, a);
   p = __fma_rn(p, f, 1.0);
   p *= smp_shared()->tab[n & (kSmpTab - 1)];
-  // times 2^((n >> 9) + 44) (a normal number: n >> 9 >= -61), then the integer nearest
-  const double v = __hiloint2double(__double2hiint(p) + (((n >> 9) + kSmpOneBits) << 20),
+  // times 2^(n >> 9) (a normal number: n >> 9 >= -61), then the integer nearest
+  const double v = __hiloint2double(__double2hiint(p) + (n & ~(kSmpTab - 1)) * (1 << 11),
                                     __double2loint(p));
   return static_cast<u64>(__double_as_longlong(v + 4503599627370496.0));
 }
@@ -280,28 +269,6 @@ __device__ __forceinline__ u64 smp_block_scan(u64 v) {
   return v;
 }
 
-// Falling bitonic sort of list[0..n), n <= kSmpList.
-__device__ __noinline__ void smp_sort(int n) {
-  u64* a = smp_shared()->list;
-  const int tid = threadIdx.x;
-  int n2 = 64;
-  while (n2 < n) n2 <<= 1;
-  for (int i = n + tid; i < n2; i += kSmpThreads) a[i] = 0;
-  for (int k = 2; k <= n2; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      __syncthreads();
-      for (int i = tid; i < n2 / 2; i += kSmpThreads) {
-        const int lo = 2 * i - (i & (j - 1));
-        const u64 p = a[lo], q = a[lo + j];
-        if ((p < q) == ((lo & k) == 0)) {
-          a[lo] = q;
-          a[lo + j] = p;
-        }
-      }
-    }
-  __syncthreads();
-}
-
 // The linear bin of x below the maximum: fp32 2^23 + (m - x) scale rounds to an
 // integer, and its bits order like it (a NaN comes last).
 __device__ __forceinline__ unsigned smp_bin(float m, float scale, float x) {
@@ -327,9 +294,9 @@ __device__ __forceinline__ void smp_hand_over(int which) {
     st_peer_u64(&sh->list[at + i], 0, sh->own[i]);
 }
 
-__device__ __forceinline__ void smp_clear(int bins, bool by_mass) {
+__device__ __forceinline__ void smp_clear(bool by_mass) {
   SmpShared* sh = smp_shared();
-  for (int i = threadIdx.x; i < bins; i += kSmpThreads) {
+  for (int i = threadIdx.x; i < kSmpBins; i += kSmpThreads) {
     sh->cnt[i] = 0;
     if (by_mass) {
       sh->mass[0][i] = 0;
@@ -338,39 +305,16 @@ __device__ __forceinline__ void smp_clear(int bins, bool by_mass) {
   }
   __syncthreads();
 }
+// 64-bit adds to shared memory would be a loop; two of 32 bits and a carry are not.
+__device__ __forceinline__ void smp_add(unsigned* lo, unsigned* hi, u64 w) {
+  const unsigned l = static_cast<unsigned>(w);
+  const unsigned old = atomicAdd(lo, l);
+  atomicAdd(hi, static_cast<unsigned>(w >> 32) + (old + l < old ? 1u : 0u));
+}
 __device__ __forceinline__ void smp_count(unsigned b, bool by_mass, u64 w) {
   SmpShared* sh = smp_shared();
-  if (by_mass) {
-    const unsigned lo = static_cast<unsigned>(w);
-    const unsigned old = atomicAdd(&sh->mass[0][b], lo);
-    const unsigned hi = static_cast<unsigned>(w >> 32) + (old + lo < old ? 1u : 0u);
-    if (hi) atomicAdd(&sh->mass[1][b], hi);
-  }
+  if (by_mass) smp_add(&sh->mass[0][b], &sh->mass[1][b], w);
   atomicAdd(&sh->cnt[b], 1u);
-}
-
-// Sums over the ranks of four neighbouring bins, all loads in flight at once:
-// f32(e, sum) and f64(e, sum) get bin e's, which fits either.
-template <class F32, class F64>
-__device__ __forceinline__ void smp_bins_of_all(const unsigned* bins, int ranks, F32 f32,
-                                                F64 f64) {
-  uint4 n[kSmpMaxCluster];
-#pragma unroll
-  for (int k = 0; k < kSmpMaxCluster; ++k)
-    n[k] = k < ranks ? ld_peer_v4(bins, k) : make_uint4(0, 0, 0, 0);
-  u64 t[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int k = 0; k < kSmpMaxCluster; ++k) {
-    t[0] += n[k].x;
-    t[1] += n[k].y;
-    t[2] += n[k].z;
-    t[3] += n[k].w;
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f32(e, static_cast<unsigned>(t[e]));
-    f64(e, t[e]);
-  }
 }
 
 struct SmpHit {
@@ -379,79 +323,169 @@ struct SmpHit {
   u64 all;           // the measure of all bins
   u64 upto;          // tokens before and in it
 };
-// Rank 0: the last bin that holds anything and starts before the goal - the one in
-// which it is reached, or, if rounding lets none reach it, the last of all.
-// Bins are taken in rising order, or (falling) from the last one down.  With
-// top_p >= 0 the goal becomes top_p of all.
-template <int BINS>
-__device__ SmpHit smp_merge(const SmpRow& r, bool by_mass, bool falling, u64 base, double top_p,
-                            double& goal) {
+// The cluster's histograms together: the bin in which `base` and the running
+// measure (weights, or tokens) reach the goal, or, if they never do, the last
+// that holds anything.  Bins are taken in rising order, or (falling) from the
+// last one down.  With top_p >= 0 the goal becomes top_p of all.  Each thread
+// merges one bin over the CTAs; begins and ends with a cluster barrier, behind
+// which every CTA has the answer.
+__device__ __noinline__ SmpHit smp_find(int rank, bool by_mass, bool falling, u64 base,
+                                        double top_p, double* goal_io) {
   SmpShared* sh = smp_shared();
   const int tid = threadIdx.x;
-  constexpr int kPer = BINS / kSmpThreads;   // bins of a thread, a multiple of four
-  u64 v[kPer];
-  unsigned c[kPer];
+  cluster_sync();
+  const int at = rank * kSmpThreads + tid;
+  const int b = falling ? kSmpBins - 1 - at : at;
+  unsigned n[3][kSmpRanks];
 #pragma unroll
-  for (int q = 0; q < kPer; q += 4) {
-    const int b = (falling ? BINS - kPer - tid * kPer : tid * kPer) + q;
-    smp_bins_of_all(&sh->cnt[b], r.ranks, [&](int e, unsigned n) {
-      c[q + e] = n;
-    }, [&](int e, u64 n) { v[q + e] = n; });
-    if (by_mass) {
-      smp_bins_of_all(&sh->mass[0][b], r.ranks, [&](int, unsigned) {},
-                      [&](int e, u64 n) { v[q + e] = n; });
-      smp_bins_of_all(&sh->mass[1][b], r.ranks, [&](int, unsigned) {},
-                      [&](int e, u64 n) { v[q + e] += n << 32; });
-    }
+  for (int k = 0; k < kSmpRanks; ++k) {
+    n[0][k] = ld_peer_u32(&sh->cnt[b], k);
+    n[1][k] = by_mass ? ld_peer_u32(&sh->mass[0][b], k) : 0u;
+    n[2][k] = by_mass ? ld_peer_u32(&sh->mass[1][b], k) : 0u;
   }
-  u64 sum = 0;
+  u64 c = 0, v = 0;
 #pragma unroll
-  for (int q = 0; q < kPer; ++q) sum += v[q];
-  u64 run = smp_block_scan(sum);
-  u64 tokens = 0;
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) tokens += c[q];
-  tokens = smp_block_scan(tokens) - tokens;
-  if (tid == kSmpThreads - 1) sh->bcast[0] = run;
-  if (tid == 0) sh->bcast[1] = 0;
-  __syncthreads();
+  for (int k = 0; k < kSmpRanks; ++k) {
+    c += n[0][k];
+    v += n[1][k] + (static_cast<u64>(n[2][k]) << 32);
+  }
+  if (!by_mass) v = c;
+  const u64 run_v = smp_block_scan(v), run_c = smp_block_scan(c);
+  if (tid == kSmpThreads - 1)
+    for (int k = 0; k < kSmpRanks; ++k) {
+      st_peer_u64(&sh->all_in[0][rank], k, run_v);
+      st_peer_u64(&sh->all_in[1][rank], k, run_c);
+    }
+  cluster_sync();
   SmpHit h;
-  h.all = sh->bcast[0];
-  if (top_p >= 0.0) goal = fmax(top_p * static_cast<double>(h.all), 1.0);   // the first is kept
-  run += base - sum;
-  int hit = -1;
-  u64 hit_base = 0, hit_cnt = 0, hit_upto = 0;
+  u64 before = base + run_v - v, upto = run_c, all_c = 0;
+  h.all = 0;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int q = falling ? kPer - 1 - j : j;
-    tokens += c[q];
-    if (c[q] && static_cast<double>(run) < goal) {
-      hit = (falling ? BINS - kPer - tid * kPer : tid * kPer) + q;
-      hit_base = run;
-      hit_cnt = c[q];
-      hit_upto = tokens;
+  for (int k = 0; k < kSmpRanks; ++k) {
+    if (k < rank) {
+      before += sh->all_in[0][k];
+      upto += sh->all_in[1][k];
     }
-    run += v[q];
+    h.all += sh->all_in[0][k];
+    all_c += sh->all_in[1][k];
   }
-  if (hit >= 0)
-    atomicMax(&sh->bcast[1], (static_cast<u64>(tid + 1) << 32) | static_cast<u64>(hit));
-  __syncthreads();
-  const u64 best = sh->bcast[1];
-  if (static_cast<int>(best >> 32) == tid + 1) {
-    sh->bcast[2] = hit_base;
-    sh->bcast[3] = hit_cnt;
-    sh->bcast[4] = hit_upto;
+  double goal = *goal_io;
+  if (top_p >= 0.0) *goal_io = goal = fmax(top_p * static_cast<double>(h.all), 1.0);   // keep one
+  if (c && static_cast<double>(before) < goal &&
+      (static_cast<double>(before + v) >= goal || upto == all_c)) {
+    for (int k = 0; k < kSmpRanks; ++k) {
+      st_peer_u64(&sh->hit[0], k, b);
+      st_peer_u64(&sh->hit[1], k, before);
+      st_peer_u64(&sh->hit[2], k, c);
+      st_peer_u64(&sh->hit[3], k, upto);
+    }
   }
-  __syncthreads();
-  h.bin = static_cast<unsigned>(best);
-  h.base = sh->bcast[2];
-  h.cnt = sh->bcast[3];
-  h.upto = sh->bcast[4];
+  cluster_sync();
+  h.bin = static_cast<unsigned>(sh->hit[0]);
+  h.base = sh->hit[1];
+  h.cnt = sh->hit[2];
+  h.upto = sh->hit[3];
   return h;
 }
-// Rank 0 tells every CTA; read as sh->told behind the next cluster barrier.
-__device__ __forceinline__ void smp_tell(const SmpRow& r, u64 v) {
-  if (threadIdx.x < r.ranks) st_peer_u64(&smp_shared()->told, threadIdx.x, v);
+
+// Rank 0, all threads: among n listed tokens in the order of falling keys (by_id
+// false) or rising ids, the one at which `base` and the running weights w[] reach
+// the goal (pass: exceed it): its place in the list, -1 if none does; *before gets
+// the sum in front of it.  A histogram of 256 buckets over the order leaves a
+// few tokens that are compared with one another.
+__device__ __noinline__ int smp_cross(int n, bool by_id, bool pass, u64 base, double goal,
+                                      u64* before) {
+  SmpShared* sh = smp_shared();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // falling keys are rising complements, whose low words are the ids
+  auto order = [&](int i) -> u64 {
+    const u64 key = ~sh->list[i];
+    return by_id ? key & 0xffffffffull : key;
+  };
+  auto over = [&](u64 sum) {
+    return pass ? static_cast<double>(sum) > goal : static_cast<double>(sum) >= goal;
+  };
+  u64 lo = ~0ull, hi = 0;
+  for (int i = tid; i < n; i += kSmpThreads) {
+    const u64 o = order(i);
+    lo = min(lo, o);
+    hi = max(hi, o);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  __syncthreads();
+  if (lane == 0) {
+    sh->warp_a[warp] = lo;
+    reinterpret_cast<u64*>(sh->cnt)[warp] = hi;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSmpWarps; ++w) {
+    lo = min(lo, sh->warp_a[w]);
+    hi = max(hi, reinterpret_cast<u64*>(sh->cnt)[w]);
+  }
+  __syncthreads();
+  unsigned* sum_lo = sh->cnt + 2 * kSmpList - 2 * kSmpThreads;   // behind the bucket's room
+  unsigned* sum_hi = sum_lo + kSmpThreads;
+  sum_lo[tid] = 0;
+  sum_hi[tid] = 0;
+  if (tid == 0) {
+    sh->found = 0xffffffffu;
+    sh->n_bucket = 0;
+  }
+  __syncthreads();
+  const float per = (kSmpThreads - 0.5f) / (__ull2float_ru(hi - lo) + 1.f);
+  auto bucket = [&](int i) {
+    return min(static_cast<int>(__ull2float_rn(order(i) - lo) * per), kSmpThreads - 1);
+  };
+  for (int i = tid; i < n; i += kSmpThreads) {
+    const int b = bucket(i);
+    smp_add(&sum_lo[b], &sum_hi[b], sh->w[i]);
+  }
+  __syncthreads();
+  const u64 v = sum_lo[tid] + (static_cast<u64>(sum_hi[tid]) << 32);
+  const u64 run = base + smp_block_scan(v);
+  if (v && over(run) && !over(run - v)) {
+    sh->found = tid;
+    sh->bcast[0] = run - v;
+  }
+  __syncthreads();
+  const unsigned in = sh->found;
+  if (in == 0xffffffffu) return -1;
+  base = sh->bcast[0];
+  __syncthreads();
+  // the bucket's tokens: few, unless many keys lie together
+  constexpr int kRoom = kSmpList - kSmpThreads;
+  for (int i = tid; i < n; i += kSmpThreads)
+    if (bucket(i) == static_cast<int>(in)) {
+      const unsigned at = atomicAdd(&sh->n_bucket, 1u);
+      if (at < kRoom) sh->bucket[at] = i;
+    }
+  if (tid == 0) sh->found = 0xffffffffu;
+  __syncthreads();
+  const unsigned nb = sh->n_bucket;
+  const bool listed = nb <= kRoom;
+  const int m = listed ? static_cast<int>(nb) : n;
+  for (int a = tid; a < m; a += kSmpThreads) {
+    const int i = listed ? static_cast<int>(sh->bucket[a]) : a;
+    if (bucket(i) != static_cast<int>(in) || sh->w[i] == 0) continue;
+    const u64 o = order(i);
+    u64 sum = base;
+    for (int c = 0; c < m; ++c) {
+      const int j = listed ? static_cast<int>(sh->bucket[c]) : c;
+      if ((listed || bucket(j) == static_cast<int>(in)) && order(j) < o) sum += sh->w[j];
+    }
+    if (over(sum + sh->w[i]) && !over(sum)) {
+      sh->found = i;
+      sh->bcast[0] = sum;
+    }
+  }
+  __syncthreads();
+  *before = sh->bcast[0];
+  return static_cast<int>(sh->found);
 }
 
 // The border of a kept prefix among the tokens with key >= floor_key: the key
@@ -467,13 +501,13 @@ __device__ __noinline__ u64 smp_border_radix(const SmpRow r, bool by_mass, u64 f
   SmpShared* sh = smp_shared();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t prefix = 0;
-  u64 base = 0;             // rank 0: tokens, or weight, above the current prefix
-  u64 ties = 0;             // rank 0: tokens of the final value
+  u64 base = 0;             // tokens, or weight, above the current prefix
+  u64 ties = 0;             // tokens of the final value
   double goal = static_cast<double>(want);
   for (int level = 0; level < 3; ++level) {
     const int bits = level == 2 ? 10 : 11;
     const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
-    smp_clear(kSmpRadix, by_mass);
+    smp_clear(by_mass);
     smp_each(r, [&](const float (&raw)[4], int i) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -487,32 +521,24 @@ __device__ __noinline__ u64 smp_border_radix(const SmpRow r, bool by_mass, u64 f
         smp_count((o >> shift) & ((1u << bits) - 1), by_mass, w);
       }
     });
-    cluster_sync();
-    if (r.rank == 0) {
-      const SmpHit h = smp_merge<kSmpRadix>(r, by_mass, true, base,
-                                            by_mass && level == 0 ? top_p : -1.0, goal);
-      base = h.base;
-      ties = h.cnt;
-      smp_tell(r, h.bin);
-    }
-    cluster_sync();
-    prefix = (prefix << bits) | static_cast<uint32_t>(sh->told);
+    const SmpHit h = smp_find(r.rank, by_mass, true, base, by_mass && level == 0 ? top_p : -1.0,
+                              &goal);
+    base = h.base;
+    ties = h.cnt;
+    prefix = (prefix << bits) | h.bin;
   }
   // all tokens of this value weigh the same: how many of them are kept
-  if (r.rank == 0) {
-    u64 n_keep;
-    if (by_mass) {
-      const u64 w = smp_weight(r, smp_value(prefix));
-      const double over = (goal - static_cast<double>(base)) / static_cast<double>(w);
-      n_keep = over >= static_cast<double>(ties) ? ties : static_cast<u64>(over);
-      while (n_keep < ties && static_cast<double>(base + n_keep * w) < goal) ++n_keep;
-      while (n_keep > 1 && static_cast<double>(base + (n_keep - 1) * w) >= goal) --n_keep;
-    } else {
-      n_keep = want - base;
-    }
-    n_keep = max(1ull, min(ties, n_keep));
-    if (tid < r.ranks) st_peer_u64(&sh->n_keep, tid, n_keep);
+  u64 n_keep;
+  if (by_mass) {
+    const u64 w = smp_weight(r, smp_value(prefix));
+    const double over = (goal - static_cast<double>(base)) / static_cast<double>(w);
+    n_keep = over >= static_cast<double>(ties) ? ties : static_cast<u64>(over);
+    while (n_keep < ties && static_cast<double>(base + n_keep * w) < goal) ++n_keep;
+    while (n_keep > 1 && static_cast<double>(base + (n_keep - 1) * w) >= goal) --n_keep;
+  } else {
+    n_keep = want - base;
   }
+  n_keep = max(1ull, min(ties, n_keep));
   // the n_keep-th tie in vocabulary order: warps own runs of the slice
   const int seg = ((r.len + kSmpWarps - 1) / kSmpWarps + 31) / 32 * 32;
   const int beg = min(r.len, warp * seg), end = min(r.len, beg + seg);
@@ -527,9 +553,8 @@ __device__ __noinline__ u64 smp_border_radix(const SmpRow r, bool by_mass, u64 f
   const u64 upto = smp_block_scan(lane == 0 ? in_warp : 0ull);
   const u64 warp_end = __shfl_sync(0xffffffffu, upto, 0);
   if (tid == kSmpThreads - 1)
-    for (int k = 0; k < r.ranks; ++k) st_peer_u64(&sh->ties_in[which][r.rank], k, upto);
+    for (int k = 0; k < kSmpRanks; ++k) st_peer_u64(&sh->ties_in[which][r.rank], k, upto);
   cluster_sync();
-  const u64 n_keep = sh->n_keep;
   u64 at = warp_end - in_warp;
   for (int k = 0; k < r.rank; ++k) at += sh->ties_in[which][k];
   if (at < n_keep && n_keep <= at + in_warp) {
@@ -540,7 +565,7 @@ __device__ __noinline__ u64 smp_border_radix(const SmpRow r, bool by_mass, u64 f
       const unsigned b = __ballot_sync(0xffffffffu, tie);
       const u64 rank_here = at + __popc(b & ((1u << lane) - 1)) + 1;
       if (tie && rank_here == n_keep)
-        for (int k = 0; k < r.ranks; ++k) st_peer_u64(&sh->border[which], k, key);
+        for (int k = 0; k < kSmpRanks; ++k) st_peer_u64(&sh->border[which], k, key);
       at += __popc(b);
     }
   }
@@ -549,13 +574,14 @@ __device__ __noinline__ u64 smp_border_radix(const SmpRow r, bool by_mass, u64 f
 }
 
 // Tokens of one bin of a histogram into rank 0's list, and of them the border:
-// the first at which `base` and their running measure reach the goal (base and
-// goal are rank 0's).
+// the first at which `base` and their running measure reach the goal.
 template <class BinAt>
 __device__ __forceinline__ u64 smp_border_in_bin(const SmpRow& r, BinAt bin_at, unsigned bin,
                                                  bool by_mass, u64 base, double goal, int which) {
   SmpShared* sh = smp_shared();
   const int tid = threadIdx.x;
+  if (tid == 0) sh->n_own = 0;
+  __syncthreads();
   smp_each(r, [&](const float (&x)[4], int i) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -565,89 +591,71 @@ __device__ __forceinline__ u64 smp_border_in_bin(const SmpRow& r, BinAt bin_at, 
   cluster_sync();
   if (r.rank == 0) {
     const int n = min(sh->n_list[1 + which], static_cast<unsigned>(kSmpList));
-    smp_sort(n);
-    constexpr int kPer = kSmpList / kSmpThreads;
-    const int i0 = kPer * tid;
-    u64 w[kPer], sum = 0;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      w[q] = i0 + q < n ? (by_mass ? smp_weight(r, smp_key_value(sh->list[i0 + q])) : 1ull) : 0ull;
-      sum += w[q];
-    }
-    u64 at = base + smp_block_scan(sum) - sum;
-    if (tid == 0) sh->first_bad = 0;
+    for (int i = tid; i < n; i += kSmpThreads)
+      sh->w[i] = by_mass ? smp_weight(r, smp_key_value(sh->list[i])) : 1ull;
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      if (w[q] && static_cast<double>(at) < goal) atomicMax(&sh->first_bad, i0 + q);
-      at += w[q];
-    }
-    __syncthreads();
-    if (tid < r.ranks) st_peer_u64(&sh->border[which], tid, sh->list[sh->first_bad]);
+    u64 before;
+    const int at = smp_cross(n, false, false, base, goal, &before);
+    if (tid < kSmpRanks) st_peer_u64(&sh->border[which], tid, at >= 0 ? sh->list[at] : 0ull);
   }
   cluster_sync();
   return sh->border[which];
 }
 
-// What rank 0 tells besides a bin.
-constexpr u64 kSmpRefine = 1ull << 32, kSmpNothing = 2ull << 32;
+// Bins of a search's two levels: of m - x below the maximum, then the parts of
+// the bin in which the border lies.
+struct SmpBinning {
+  float m, scale, shift;
+  unsigned bin;
+  int level;
+  // kSmpBins or more: not looked at
+  __device__ __forceinline__ unsigned operator()(float x) const {
+    const unsigned b = smp_bin(m, scale, x);
+    if (level == 0) return b;
+    if (b != bin) return kSmpBins;
+    const float f = fmaxf(fmaf(m - x, scale, -shift), 0.f);   // 0 .. 1
+    return min(__float_as_uint(fmaf(f, kSmpBins - 2.f, 8388608.f)) - 0x4B000000u, kSmpBins - 1u);
+  }
+  __device__ __forceinline__ void refine(unsigned b) {
+    bin = b;
+    shift = static_cast<float>(b) - 0.5f;
+    level = 1;
+  }
+};
 
 // The border of top_k = want: a histogram of linear bins below the maximum, of
 // the bin in which the border lies if that holds more than a list, and the
-// sorted list.  The radix search where even that holds more (ties).
+// listed tokens themselves.  The radix search where even that holds more (ties).
 __device__ __noinline__ u64 smp_border_k(const SmpRow r, float scale, u64 want) {
   SmpShared* sh = smp_shared();
   if (!r.fast) return smp_border_radix(r, false, 0ull, want, 0.0, 0);
-  unsigned bin = 0;
-  float shift = 0.f;         // second level: (m - x) scale - shift spans [0, 1]
-  u64 base = 0;              // rank 0
+  SmpBinning bins = {r.m, scale, 0.f, 0u, 0};
+  u64 base = 0;
   double goal = static_cast<double>(want);
-  int level = 0;
-  // kSmpBins or more: not looked at
-  auto bin_at = [&](float x, int) -> unsigned {
-    const unsigned b = smp_bin(r.m, scale, x);
-    if (level == 0) return b;
-    if (b != bin) return kSmpBins;
-    const float f = fmaxf(fmaf(r.m - x, scale, -shift), 0.f);
-    return min(__float_as_uint(fmaf(f, kSmpBins - 2.f, 8388608.f)) - 0x4B000000u, kSmpBins - 1u);
-  };
-  for (;; ++level) {
-    smp_clear(kSmpBins, false);
-    smp_each(r, [&](const float (&x)[4], int i) {
+  for (;;) {
+    smp_clear(false);
+    smp_each(r, [&](const float (&x)[4], int) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const unsigned b = bin_at(x[q], i + q);
+        const unsigned b = bins(x[q]);
         if (b < kSmpBins) atomicAdd(&sh->cnt[b], 1u);
       }
     });
-    cluster_sync();
-    if (r.rank == 0) {
-      const SmpHit h = smp_merge<kSmpBins>(r, false, false, base, -1.0, goal);
-      base = h.base;
-      // fewer than wanted weigh anything: nothing to cut
-      smp_tell(r, level == 0 && h.all < want ? kSmpNothing
-                  : h.cnt > kSmpList         ? kSmpRefine | h.bin
-                                             : h.bin);
-    }
-    if (threadIdx.x == 0) sh->n_own = 0;
-    cluster_sync();
-    const u64 told = sh->told;
-    if (told >= kSmpNothing) return 0ull;
-    if (told < kSmpRefine)
-      return smp_border_in_bin(r, bin_at, static_cast<unsigned>(told), false, base, goal, 0);
-    if (level) return smp_border_radix(r, false, 0ull, want, 0.0, 0);
-    bin = static_cast<unsigned>(told);
-    shift = static_cast<float>(bin) - 0.5f;
+    const SmpHit h = smp_find(r.rank, false, false, base, -1.0, &goal);
+    if (bins.level == 0 && h.all < want) return 0ull;   // fewer weigh anything: nothing to cut
+    base = h.base;
+    if (h.cnt <= kSmpList)
+      return smp_border_in_bin(r, [&](float x, int) { return bins(x); }, h.bin, false, base, goal,
+                               0);
+    if (bins.level) return smp_border_radix(r, false, 0ull, want, 0.0, 0);
+    bins.refine(h.bin);
   }
 }
 
-// top_p over the tokens with key >= floor_key: a histogram of their weights in
-// linear bins, of the bin in which the border lies if that holds more than a
-// list, and the sorted list.  Sums of integers are exact, so the bins say exactly
-// where the border lies.  If a list can hold all tokens up to it, the list is
-// filled (`listed` is set, rank 0 has the weight of all in mass_all) and the
-// caller draws from it.  The radix search where even the second histogram leaves
-// too many (ties).
+// top_p over the tokens with key >= floor_key: the same with their weights.  Sums
+// of integers are exact, so the bins say exactly where the border lies.  If a
+// list can hold all tokens up to it, the list is filled and the caller draws
+// from it (`listed`; mass_all is the weight of all that top_p refers to).
 __device__ __noinline__ u64 smp_border_p(const SmpRow r, float scale, u64 floor_key,
                                          double top_p, bool* listed, u64* mass_all) {
   SmpShared* sh = smp_shared();
@@ -656,67 +664,56 @@ __device__ __noinline__ u64 smp_border_p(const SmpRow r, float scale, u64 floor_
   if (!r.fast) return smp_border_radix(r, true, floor_key, 0ull, top_p, 1);
   const float tau = floor_key ? smp_key_value(floor_key) : -INFINITY;
   const int last = floor_key ? static_cast<int>(smp_id(floor_key)) - r.begin : 0x7fffffff;
-  const bool plain = floor_key == 0 && r.w_min == 0;
-  auto kept = [&](float x, int i) { return x > tau || (x == tau && i <= last); };
-  scale *= static_cast<float>(kSmpRadix / kSmpBins);    // finer bins: a weight costs more
-  unsigned bin = 0;
-  float shift = 0.f;         // second level: (m - x) scale - shift spans [0, 1]
-  int level = 0;
-  // kSmpRadix or more: not looked at
+  SmpBinning bins = {r.m, scale, 0.f, 0u, 0};
   auto bin_at = [&](float x, int i) -> unsigned {
-    const unsigned b = smp_bin(r.m, scale, x);
-    if (!plain && !kept(x, i)) return kSmpRadix;
-    if (level == 0) return b;
-    if (b != bin) return kSmpRadix;
-    const float f = fmaxf(fmaf(r.m - x, scale, -shift), 0.f);
-    return min(__float_as_uint(fmaf(f, kSmpRadix - 2.f, 8388608.f)) - 0x4B000000u,
-               kSmpRadix - 1u);
+    const unsigned b = bins(x);
+    return floor_key == 0 || x > tau || (x == tau && i <= last) ? b : kSmpBins;
   };
-  u64 base = 0;              // rank 0
+  u64 base = 0;
   double goal = 0.0;
-  for (;; ++level) {
-    smp_clear(kSmpRadix, true);
+  SmpHit h;
+  for (;;) {
+    smp_clear(true);
     smp_each(r, [&](const float (&x)[4], int i) {
       unsigned b[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) b[q] = bin_at(x[q], i + q);
-      if (min(min(b[0], b[1]), min(b[2], b[3])) >= kSmpRadix) return;
+      if (min(min(b[0], b[1]), min(b[2], b[3])) >= kSmpBins) return;
       u64 w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) w[q] = smp_bits(r, x[q]) - kSmpBias;
+      if (r.w_min) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (w[q] < r.w_min) b[q] = kSmpBins;
+      }
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (b[q] < kSmpRadix && w[q] && w[q] >= r.w_min) smp_count(b[q], true, w[q]);
+        if (b[q] < kSmpBins) smp_count(b[q], true, w[q]);
     });
-    cluster_sync();
-    if (r.rank == 0) {
-      const SmpHit h = smp_merge<kSmpRadix>(r, true, false, base, level == 0 ? top_p : -1.0, goal);
-      base = h.base;
-      if (level == 0) *mass_all = h.all;
-      smp_tell(r, level == 0 && h.upto <= kSmpList ? kSmpNothing | h.bin
-                  : h.cnt > kSmpList               ? kSmpRefine | h.bin
-                                                   : h.bin);
+    h = smp_find(r.rank, true, false, base, bins.level == 0 ? top_p : -1.0, &goal);
+    base = h.base;
+    if (bins.level == 0) {
+      *mass_all = h.all;
+      if (h.upto <= kSmpList) break;
     }
-    if (tid == 0) sh->n_own = 0;
-    cluster_sync();
-    const u64 told = sh->told;
-    bin = level == 0 ? static_cast<unsigned>(told) : bin;
-    if (told >= kSmpNothing) break;
-    if (told < kSmpRefine)
-      return smp_border_in_bin(r, bin_at, static_cast<unsigned>(told), true, base, goal, 1);
-    if (level) return smp_border_radix(r, true, floor_key, 0ull, top_p, 1);
-    shift = static_cast<float>(bin) - 0.5f;
+    if (h.cnt <= kSmpList) return smp_border_in_bin(r, bin_at, h.bin, true, base, goal, 1);
+    if (bins.level) return smp_border_radix(r, true, floor_key, 0ull, top_p, 1);
+    bins.refine(h.bin);
   }
+  if (tid == 0) sh->n_own = 0;
+  __syncthreads();
   smp_each(r, [&](const float (&x)[4], int i) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (bin_at(x[q], i + q) <= bin) smp_candidate(x[q], r.begin + i + q);
+      if (bin_at(x[q], i + q) <= h.bin) smp_candidate(x[q], r.begin + i + q);
   });
   smp_hand_over(3);
   cluster_sync();
-  // tokens of these bins that min_p filters are in the list too
-  *listed = ld_peer_u32(&sh->n_list[3], 0) <= kSmpList;
+  // more than counted only if min_p filters some of these bins' tokens
+  if (r.rank == 0 && tid < kSmpRanks) st_peer_u32(&sh->verdict, tid, sh->n_list[3] <= kSmpList);
   cluster_sync();
+  *listed = sh->verdict != 0;
   return *listed ? floor_key : smp_border_radix(r, true, floor_key, 0ull, top_p, 1);
 }
 
@@ -790,16 +787,16 @@ __device__ __forceinline__ SmpResult smp_draw_row(const SmpRow& r, u64 floor_key
     const u64 d = draft >= 0 && draft_at >= 0 && draft_at < r.len
                       ? weight(__ldg(r.x + draft_at), draft_at)
                       : 0ull;
-    for (int k = 0; k < r.ranks; ++k) {
+    for (int k = 0; k < kSmpRanks; ++k) {
       st_peer_u64(&sh->kept_in[r.rank], k, upto);
       st_peer_u64(&sh->draft_in[r.rank], k, d);
     }
   }
-  if (tid == 0) sh->first_bad = kSmpWarps;
+  if (tid == 0) sh->found = kSmpWarps;
   cluster_sync();   // the row's last: no CTA touches another's memory behind it
   u64 before = 0, total = 0, draft_w = 0;
   int draft_rank = -1;
-  for (int k = 0; k < r.ranks; ++k) {
+  for (int k = 0; k < kSmpRanks; ++k) {
     const u64 s = sh->kept_in[k], d = sh->draft_in[k];
     if (k < r.rank) before += s;
     total += s;
@@ -829,13 +826,13 @@ __device__ __forceinline__ SmpResult smp_draw_row(const SmpRow& r, u64 floor_key
   }
   if (lane == 0 && run != end_sum && !(static_cast<double>(run) > goal) &&
       static_cast<double>(end_sum) > goal) {
-    sh->first_bad = warp;
+    sh->found = warp;
     sh->bcast[0] = run;
   }
   __syncthreads();
-  if (sh->first_bad >= kSmpWarps) return out;    // not in this slice
+  if (sh->found >= kSmpWarps) return out;        // not in this slice
   // the CTA scans that run together, eight neighbours a thread
-  const int b0 = static_cast<int>(sh->first_bad) * seg, b1 = min(r.padded, b0 + seg);
+  const int b0 = static_cast<int>(sh->found) * seg, b1 = min(r.padded, b0 + seg);
   run = sh->bcast[0];
   for (int i0 = b0; i0 < b1; i0 += kSmpThreads * 4) {
     const int i = i0 + tid * 4;
@@ -948,89 +945,52 @@ __device__ __noinline__ SmpResult smp_draw_list(const SmpRow r, int n, int k, do
                                                 u64 mass_all, int draft, float u_accept, float u) {
   SmpShared* sh = smp_shared();
   const int tid = threadIdx.x;
-  constexpr int kPer = kSmpList / kSmpThreads;
   SmpResult out = {0, 0, -1, 0.f};
-  smp_sort(n);
-  if (tid == 0) {
-    sh->first_bad = n;
-    sh->bcast[2] = 0;
-  }
-  // running weights in falling order: neighbours a thread
-  const int i0 = kPer * tid;
-  u64 w[kPer], sum = 0;
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    const int i = i0 + q;
-    w[q] = i < n && (k <= 0 || i < k) ? smp_weight(r, smp_key_value(sh->list[i])) : 0ull;
-    sum += w[q];
-  }
-  u64 run = smp_block_scan(sum);
-  if (tid == kSmpThreads - 1) sh->bcast[0] = run;
+  u64 floor_key = 0, before;
+  for (int i = tid; i < n; i += kSmpThreads) sh->w[i] = 1;
   __syncthreads();
-  run -= sum;
-  const double goal = top_p * static_cast<double>(mass_all ? mass_all : sh->bcast[0]);
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    const int i = i0 + q;
-    if (i < n && i > 0 && (w[q] == 0 || !(static_cast<double>(run) < goal)))
-      atomicMin(&sh->first_bad, static_cast<unsigned>(i));
-    run += w[q];
+  if (k > 0 && k < n) {
+    const int at = smp_cross(n, false, false, 0ull, static_cast<double>(k), &before);
+    floor_key = at >= 0 ? sh->list[at] : 0ull;
   }
-  __syncthreads();
-  n = sh->first_bad;            // the kept tokens are list[0 .. n)
-  // into vocabulary order
-  u64 key[kPer];
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    const int i = i0 + q;
-    key[q] = 0;
-    if (i < n) {
-      const u64 old = sh->list[i];
-      if (static_cast<int>(smp_id(old)) == draft) sh->bcast[2] = w[q];
-      key[q] = (old << 32) | (old >> 32);     // falling ~id first
+  u64 sum = 0;
+  for (int i = tid; i < n; i += kSmpThreads) {
+    const u64 w = sh->list[i] >= floor_key ? smp_weight(r, smp_key_value(sh->list[i])) : 0ull;
+    sh->w[i] = w;
+    sum += w;
+  }
+  sum = smp_block_sum(sum);
+  const double goal = fmax(top_p * static_cast<double>(mass_all ? mass_all : sum), 1.0);
+  if (goal <= static_cast<double>(sum)) {
+    const int at = smp_cross(n, false, false, 0ull, goal, &before);
+    if (at >= 0) floor_key = max(floor_key, sh->list[at]);
+  }
+  u64 draft_w = 0, total = 0;
+  for (int i = tid; i < n; i += kSmpThreads) {
+    u64 w = sh->w[i];
+    if (sh->list[i] < floor_key) w = 0;
+    if (static_cast<int>(smp_id(sh->list[i])) == draft) {
+      draft_w = w;
+      w = 0;
     }
+    sh->w[i] = w;
+    total += w;
   }
-  __syncthreads();
-#pragma unroll
-  for (int q = 0; q < kPer; ++q)
-    if (i0 + q < n) sh->list[i0 + q] = key[q];
-  smp_sort(n);
-  const u64 draft_w = sh->bcast[2];
-  int id[kPer];
-  sum = 0;
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    const int i = i0 + q;
-    key[q] = i < n ? sh->list[i] : 0;
-    id[q] = static_cast<int>(0xffffffffu - static_cast<uint32_t>(key[q] >> 32));
-    w[q] = i < n ? smp_weight(r, smp_value(static_cast<uint32_t>(key[q]))) : 0;
-    if (id[q] == draft) w[q] = 0;
-    sum += w[q];
-  }
-  run = smp_block_scan(sum);
-  if (tid == kSmpThreads - 1) sh->bcast[1] = run;
-  __syncthreads();
-  const u64 total = sh->bcast[1];             // without the draft
+  total = smp_block_sum(total);             // without the draft
+  draft_w = smp_block_sum(draft_w);
   if (smp_accepts(draft_w, total + draft_w, u_accept)) {
     out.writer = tid == 0;
     out.accepted = 1;
     out.token = draft;
     return out;
   }
-  if (total == 0) {
-    out.writer = tid == 0;
-    return out;
-  }
-  run -= sum;
-  const double at = static_cast<double>(smp_unit(u)) * static_cast<double>(total);
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    if (w[q] && !(static_cast<double>(run) > at) && static_cast<double>(run + w[q]) > at) {
-      out.writer = 1;
-      out.token = id[q];
-      out.prob = smp_share(w[q], total);
-    }
-    run += w[q];
+  out.writer = tid == 0;
+  if (total == 0) return out;
+  const int at = smp_cross(n, true, true, 0ull,
+                           static_cast<double>(smp_unit(u)) * static_cast<double>(total), &before);
+  if (at >= 0) {
+    out.token = static_cast<int>(smp_id(sh->list[at]));
+    out.prob = smp_share(sh->w[at], total);
   }
   return out;
 }
@@ -1044,7 +1004,6 @@ __device__ __forceinline__ SmpResult smp_row(const float* row, int V, int slice,
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   SmpRow r;
   r.rank = static_cast<int>(cluster_rank());
-  r.ranks = gridDim.x;
   r.begin = r.rank * slice;
   r.len = max(0, min(V - r.begin, slice));
   r.padded = (r.len + 127) & ~127;
@@ -1072,12 +1031,13 @@ __device__ __forceinline__ SmpResult smp_row(const float* row, int V, int slice,
   const bool by_k = k_in > 0 && k_in < V;
   const bool by_p = p_in < 1.f;
   const double top_p = p_in > 0.f ? static_cast<double>(p_in) : 0.0;
-  const float scale = fminf((kSmpBins - 1) / (kSmpReach * T), 3e38f);
+  const float scale = fminf((kSmpMaxBins - 1) / (kSmpReach * T), 3e38f);
+  const float fine = fminf((kSmpBins - 1) / (kSmpReach * T), 3e38f);
   const bool by_list = !greedy && by_k && k_in <= kSmpListTopK;
   if (!greedy) {
-    for (int i = tid; i < kSmpTab; i += kSmpThreads) sh->tab[i] = exp2(i * (1.0 / kSmpTab));
+    for (int i = tid; i < kSmpTab; i += kSmpThreads) sh->tab[i] = exp2(kSmpOneBits + i * (1.0 / kSmpTab));
     if (by_list)
-      for (int i = tid; i < kSmpBins; i += kSmpThreads) sh->cnt[i] = 0;
+      for (int i = tid; i < kSmpMaxBins; i += kSmpThreads) sh->cnt[i] = 0;
   }
   if (tid < 4) sh->n_list[tid] = 0;
   if (tid < 4) sh->thr[tid] = -INFINITY;
@@ -1097,9 +1057,9 @@ __device__ __forceinline__ SmpResult smp_row(const float* row, int V, int slice,
     // thr[j]: a value that at least aim / 2^j of the slice's tokens reach, seen
     // from the threads' maxima alone (-inf where too few are within reach)
     const unsigned b = smp_bin(top, scale, mine);
-    if (b < kSmpBins) atomicAdd(&sh->cnt[b], 1u);
+    if (b < kSmpMaxBins) atomicAdd(&sh->cnt[b], 1u);
     __syncthreads();
-    constexpr int kPer = kSmpBins / kSmpThreads;
+    constexpr int kPer = kSmpMaxBins / kSmpThreads;
     unsigned c[kPer], sum = 0;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
@@ -1134,7 +1094,7 @@ __device__ __forceinline__ SmpResult smp_row(const float* row, int V, int slice,
     }
     __syncthreads();
   }
-  if (tid < r.ranks) {
+  if (tid < kSmpRanks) {
     st_peer_u32(&sh->top_in[r.rank], tid, __float_as_uint(top));
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -1146,9 +1106,9 @@ __device__ __forceinline__ SmpResult smp_row(const float* row, int V, int slice,
   float cut = -INFINITY;
   {
     const int c = lane >> 2, j = lane & 3;
-    top = lane < r.ranks ? sh->top_in[lane] : -INFINITY;
+    top = lane < kSmpRanks ? sh->top_in[lane] : -INFINITY;
     if (by_list) {
-      const float v = c < r.ranks ? sh->thr_in[c][j] : -INFINITY;
+      const float v = c < kSmpRanks ? sh->thr_in[c][j] : -INFINITY;
       int above = 0;
 #pragma unroll
       for (int o = 1; o < 8; ++o) {
@@ -1181,7 +1141,7 @@ __device__ __forceinline__ SmpResult smp_row(const float* row, int V, int slice,
     if (tid == 0) st_peer_u32(&sh->first_in[r.rank], 0, sh->first);
     cluster_sync();
     unsigned id = 0xffffffffu;
-    for (int k = 0; k < r.ranks; ++k) id = min(id, sh->first_in[k]);
+    for (int k = 0; k < kSmpRanks; ++k) id = min(id, sh->first_in[k]);
     out.token = static_cast<int>(id);
     out.accepted = out.token == draft;
     out.prob = 1.f;
@@ -1211,13 +1171,13 @@ __device__ __forceinline__ SmpResult smp_row(const float* row, int V, int slice,
     }
     smp_hand_over(0);
     cluster_sync();
-    if (r.rank == 0 && tid < r.ranks) st_peer_u32(&sh->verdict, tid, sh->n_list[0] <= kSmpList);
+    if (r.rank == 0 && tid < kSmpRanks) st_peer_u32(&sh->verdict, tid, sh->n_list[0] <= kSmpList);
     cluster_sync();
     listed = sh->verdict != 0;
   }
   if (!listed) {
-    if (by_k) floor_key = smp_border_k(r, scale, static_cast<u64>(k_in));
-    if (by_p) floor_key = smp_border_p(r, scale, floor_key, top_p, &listed, &mass_all);
+    if (by_k) floor_key = smp_border_k(r, fine, static_cast<u64>(k_in));
+    if (by_p) floor_key = smp_border_p(r, fine, floor_key, top_p, &listed, &mass_all);
   }
   if (!listed) return smp_draw_row(r, floor_key, draft, u_accept, u);
   out.writer = 0;
@@ -1267,61 +1227,49 @@ struct VerifySampledParams {
   unsigned* done;         // [B] rows of the request that are settled (zeroed before)
   unsigned* refused;      // [B] K + 1 - (first refused row), 0: none yet (zeroed before)
   int32_t* row_token;     // [B][K + 1] what a row would emit if it is the last
-  int run;                // rows that one cluster settles in turn
 };
 
-// Cluster (y, z) settles rows [z * run, ..) of request y in turn, until one
-// refuses its draft.  Clusters start in the order of z: when a late one starts,
-// an earlier row of its request may have refused, and its rows have nothing to
-// say.  Whether it looks only decides if work is saved: a request's answer is
-// its first refusing row's, whoever ran.  The cluster that settles a request's
-// last rows writes the answer.
+// Cluster (y, z) settles row z of request y.  Clusters start in the order of z:
+// when a late one starts, an earlier row of its request may have refused, and
+// the row has nothing to say.  Whether it looks only decides if work is saved: a
+// request's answer is its first refusing row's, whoever ran.  The cluster that
+// settles a request's last row writes the answer.  (Runs of two, four or eight
+// rows a cluster, which spare launches, were slower: 128 requests of 16 rows 354,
+// 391 and 413 us against 272, for the rows of one request then wait in line.)
 __global__ void __launch_bounds__(kSmpThreads, kSmpCtas)
 verify_sampled_kernel(const VerifySampledParams p) {
   pdl_trigger();
   pdl_wait();
   SmpShared* sh = smp_shared();
-  const int b = blockIdx.y, K = p.K;
-  const int first = blockIdx.z * p.run, end = min(K + 1, first + p.run);
+  const int b = blockIdx.y, i = blockIdx.z, K = p.K;
   const bool lead = threadIdx.x == 0 && cluster_rank() == 0;
   bool needed = true;
-  if (first > 0) {
+  if (i > 0) {
     // one reading for the whole cluster: rank 0's
     if (lead) {
       const unsigned refused = *reinterpret_cast<volatile unsigned*>(p.refused + b);
-      const unsigned told = !(refused && first > K + 1 - static_cast<int>(refused));
-      for (unsigned k = 0; k < gridDim.x; ++k) st_peer_u32(&sh->verdict, k, told);
+      const unsigned told = !(refused && i > K + 1 - static_cast<int>(refused));
+      for (unsigned k = 0; k < kSmpRanks; ++k) st_peer_u32(&sh->more, k, told);
     }
     cluster_sync();
-    needed = sh->verdict != 0;
-    __syncthreads();
+    needed = sh->more != 0;
   }
-  for (int i = first; needed && i < end; ++i) {
+  if (needed) {
     const int draft = i < K ? p.drafts[static_cast<int64_t>(b) * K + i] : -1;
     const SmpResult res =
-        smp_row(p.logits + (static_cast<int64_t>(b) * (K + 1) + i) * p.ld, p.V, p.slice, p.set,
-                b, draft, i < K ? p.u_accept[static_cast<int64_t>(b) * K + i] : 0.f,
-                p.u_sample[b]);
-    if (res.writer && (!res.accepted || i == K)) {
+        smp_row(p.logits + (static_cast<int64_t>(b) * (K + 1) + i) * p.ld, p.V, p.slice, p.set, b,
+                draft, i < K ? p.u_accept[static_cast<int64_t>(b) * K + i] : 0.f, p.u_sample[b]);
+    if (!res.writer) return;
+    if (!res.accepted || i == K) {
       p.row_token[static_cast<int64_t>(b) * (K + 1) + i] = res.token;
       __threadfence();
       atomicMax(p.refused + b, static_cast<unsigned>(K + 1 - i));
-      __threadfence();
     }
-    // whether to go on (an accepted draft's writer is the leader); behind the
-    // barrier the row's stores are out, for the leader to count it as settled
-    if (lead) {
-      const unsigned more = res.writer && res.accepted && i < K;
-      for (unsigned k = 0; k < gridDim.x; ++k) st_peer_u32(&sh->told32, k, more);
-    }
-    cluster_sync();
-    needed = sh->told32 != 0;
-    cluster_sync();      // read by all before anything is written again
+  } else if (!lead) {
+    return;
   }
-  if (!lead) return;
   __threadfence();
-  const unsigned mine = static_cast<unsigned>(end - first);
-  if (atomicAdd(p.done + b, mine) + mine != static_cast<unsigned>(K + 1)) return;
+  if (atomicAdd(p.done + b, 1u) != static_cast<unsigned>(K)) return;
   __threadfence();
   const int n = K + 1 - static_cast<int>(*reinterpret_cast<volatile unsigned*>(p.refused + b));
   const int32_t last =
