@@ -51,6 +51,8 @@ int sample_slice(int V) { return (cdiv(V, kSmpRanks) + 3) / 4 * 4; }
 struct PrefixPlan {
   int nt = 1, kt = 64;           // the prefix's kernel
   int tpt = 0, row_groups = 0, items = 0, tiles = 0, ctas = 0, max_segs = 0;
+  int64_t run = 1;               // (item, tile) units of a CTA
+  bool too_many = false;         // units past 31 bits
   int chunk = 0, splits = 0, R = 0;
   size_t off_ml = 0, off_own = 0, off_own_ml = 0, total = 0;
 };
@@ -71,9 +73,10 @@ PrefixPlan plan_prefix(const dflash_handle* h, int B, int q_len, int W, int pref
     p.tiles = cdiv(prefix_pages * 16, p.kt);
     const int64_t units = static_cast<int64_t>(p.items) * p.tiles;
     const int slots = p.nt == 2 ? h->num_sms : 2 * h->num_sms;
-    p.ctas = static_cast<int>(std::min<int64_t>(slots, (units + 1) / 2));
-    const int64_t longest = (units + p.ctas - 1) / p.ctas;
-    p.max_segs = static_cast<int>((longest - 1) / p.tiles + 2);
+    p.too_many = units > INT32_MAX;
+    p.run = std::max<int64_t>(2, (units + slots - 1) / slots);
+    p.ctas = static_cast<int>((units + p.run - 1) / p.run);
+    p.max_segs = static_cast<int>((p.run - 1) / p.tiles + 2);
   }
   const int own_keys = (W - prefix_pages) * 16;
   if (own_keys > 0) {
@@ -236,6 +239,7 @@ dflash_status dflash_prefix_attention(dflash_handle* h, const void* q, int q_len
   if (static_cast<int64_t>(num_pages) * c.n_kv_heads * 16 > INT32_MAX)
     return DFLASH_ERR_UNSUPPORTED_SHAPE;   // rows of the pools' tensor maps
   const PrefixPlan pl = plan_prefix(h, B, q_len, max_pages_per_seq, prefix_pages);
+  if (pl.too_many) return DFLASH_ERR_UNSUPPORTED_SHAPE;
   if (workspace_bytes < pl.total) return DFLASH_ERR_WORKSPACE;
   DF_CUDA(use_device(h->device));
   PartParams p;
@@ -255,6 +259,7 @@ dflash_status dflash_prefix_attention(dflash_handle* h, const void* q, int q_len
   p.prefix_ctas = pl.ctas;
   p.prefix_items = pl.items;
   p.prefix_tiles = pl.tiles;
+  p.prefix_run = static_cast<unsigned>(pl.run);
   p.row_groups = pl.row_groups;
   p.max_segs = pl.max_segs;
   p.prefix_o = at<float>(workspace, 0);

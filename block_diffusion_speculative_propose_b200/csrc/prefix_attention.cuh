@@ -15,13 +15,13 @@
 // the K/V tiles of KT keys that pass through a ring in shared memory; S and,
 // in its place, P (bf16) stay in tensor memory beside O:
 //   warp 0      TMA producer: lane j loads page j % (KT / 16), column half j / ..
-//   warp 1      MMA issuer (one thread): S_i = Q_i K^T, O_i += P_i V with P_i
-//               read from tensor memory
+//   warp 1      MMA issuer (one thread): S = Q K^T, O += P V with P read from
+//               tensor memory
 //   then 4 warps for each row tile: thread = row, so the maximum, the sum and
 //               the mask of a row need no exchange
-// The issue order PV_0(t) S_0(t+1) PV_1(t) S_1(t+1) keeps the tensor cores on one
-// tile while the other one's softmax runs (NT = 2); with NT = 1 two CTAs an SM
-// do the same for one another.
+// NT = 2: the issue order PV_0(t) S_0(t+1) PV_1(t) S_1(t+1) keeps the tensor cores
+// on one row tile while the other one's softmax runs.  NT = 1: S has two buffers,
+// S(t+1) is issued before P V(t), and a second CTA on the SM fills the rest.
 //   NT = 2, KT = 128: one CTA an SM, 4 D x 128 flops per byte read, for many rows
 //   NT = 1, KT = 64:  two CTAs an SM, for one request's rows
 #pragma once
@@ -43,6 +43,7 @@ struct PartParams {
   // the prefix, dealt to the first prefix_ctas CTAs in equal runs of
   // (item = kv head and row tiles, key tile)
   int prefix_ctas, prefix_items, prefix_tiles, row_groups;   // row_groups = items per kv head
+  unsigned prefix_run;   // units of a CTA; all units fit 31 bits
   int max_segs;
   float* prefix_o;     // [prefix_ctas][max_segs][NT][128][D]
   float2* prefix_ml;   // [prefix_ctas][max_segs][NT][128]
@@ -68,7 +69,8 @@ struct PartCfg {
   static constexpr int kOffBar = kOffRing + NS * kTileBytes;
   static constexpr int kSmem = 1024 + kOffBar + 256;
   static constexpr int kThreads = 64 + NT * 128;
-  static constexpr int kCols = NT * (KT + D) > 256 ? 512 : NT * (KT + D) > 128 ? 256 : 128;
+  static constexpr int kUsed = 2 * KT + NT * D;            // S twice, O
+  static constexpr int kCols = kUsed > 256 ? 512 : kUsed > 128 ? 256 : 128;
   static_assert(NS >= 3, "ring");
   static_assert(kCols * kCtas <= 512, "tensor memory");
 };
@@ -89,14 +91,30 @@ __device__ __forceinline__ void part_load_3d(void* dst, const CUtensorMap* map, 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, A: 128 lanes x packed pairs.
-__device__ __forceinline__ void part_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
+// D[tmem] (+)= A * B[smem]^T, bf16 inputs; A in shared memory, or in tensor memory
+// as 128 lanes x packed pairs.  One thread issues every product, and an operation
+// of one thread takes several cycles while a 128 x 128 x 16 product takes 64: so
+// a descriptor is one addition to its low word, and what is constant is an
+// immediate.
+template <bool ACC>
+__device__ __forceinline__ void part_mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi,
+                                            uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+__device__ __forceinline__ void part_mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void part_st_x32(uint32_t taddr, const uint32_t* r) {
@@ -111,10 +129,109 @@ __device__ __forceinline__ void part_st_x32(uint32_t taddr, const uint32_t* r) {
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void part_st_x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
 // kind::f16, bf16 x bf16 -> fp32; b_mn: B is MN-major.
 __host__ __device__ constexpr uint32_t part_idesc(int M, int N, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Two floats in a 64-bit register: the FMA pipes take both in one instruction.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 part_pack(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void part_unpack(f32x2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 part_fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 part_add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float part_max3(float a, float b, float c) {   // a NaN stays
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+constexpr float kExpC0 = 0.999928074f, kExpC1 = 0.693260985f, kExpC2 = 0.242611122f,
+                kExpC3 = 0.0551716691f;
+// 2^y of a pair on the FMA pipes, y <= 2^6: 2^y = 2^n 2^f, n = rint(y), |f| <= 1/2,
+// 2^f by the cubic of least relative error there (7.5e-5, found by a Remez exchange;
+// P is rounded to bf16, 4e-3, next).  Below -126 it stays at 2^-126.
+__device__ __forceinline__ void part_exp2_pair(f32x2 y, float& a, float& b) {
+  float ya, yb;
+  part_unpack(y, ya, yb);
+  y = part_pack(fmaxf(ya, -126.f), fmaxf(yb, -126.f));
+  const f32x2 magic = part_pack(12582912.f, 12582912.f);   // 1.5 2^23
+  const f32x2 unmagic = part_pack(-12582912.f, -12582912.f);
+  const f32x2 n = part_add2(y, magic);
+  const f32x2 whole = part_add2(n, unmagic);
+  const f32x2 f = part_fma2(whole, part_pack(-1.f, -1.f), y);
+  f32x2 p = part_pack(kExpC3, kExpC3);
+  p = part_fma2(p, f, part_pack(kExpC2, kExpC2));
+  p = part_fma2(p, f, part_pack(kExpC1, kExpC1));
+  p = part_fma2(p, f, part_pack(kExpC0, kExpC0));
+  float na, nb, pa, pb;
+  part_unpack(n, na, nb);
+  part_unpack(p, pa, pb);
+  a = __int_as_float(__float_as_int(pa) + (__float_as_int(na) << 23));
+  b = __int_as_float(__float_as_int(pb) + (__float_as_int(nb) << 23));
+}
+
+// P = 2^(s scale - ref) in the place of a row's KT scores, as bf16 pairs; returns
+// the row's sum.  In chunks of 32 scores: chunk c is read from columns 32 c ..
+// and written to columns 16 c .., never ahead of what is still to be read.
+template <int KT, bool FAST>
+__device__ __forceinline__ float part_weights(uint32_t s_at, float scale, float ref, int left) {
+  const f32x2 sc2 = part_pack(scale, scale), nr2 = part_pack(-ref, -ref);
+  f32x2 l2[2] = {part_pack(0.f, 0.f), part_pack(0.f, 0.f)};
+  float x[2][32];
+  tmem_ld_32x32b_x32(s_at, x[0]);
+  tmem_ld_wait();
+#pragma unroll
+  for (int c = 0; c < KT / 32; ++c) {
+    if (c + 1 < KT / 32) tmem_ld_32x32b_x32(s_at + (c + 1) * 32, x[(c + 1) & 1]);
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float a = x[c & 1][2 * e], b = x[c & 1][2 * e + 1];
+      if (!FAST) {
+        if (c * 32 + 2 * e >= left) a = -INFINITY;
+        if (c * 32 + 2 * e + 1 >= left) b = -INFINITY;
+      }
+      const f32x2 y = part_fma2(part_pack(a, b), sc2, nr2);
+      if (FAST && (e & 3) == 3) {
+        part_exp2_pair(y, a, b);
+      } else {
+        part_unpack(y, a, b);
+        a = part_ex2(a);
+        b = part_ex2(b);
+      }
+      l2[e & 1] = part_add2(l2[e & 1], part_pack(a, b));
+      w[e] = pack_bf16x2(a, b);
+    }
+    if (c + 1 < KT / 32) tmem_ld_wait();
+    part_st_x16(s_at + c * 16, w);
+  }
+  float la, lb;
+  part_unpack(part_add2(l2[0], l2[1]), la, lb);
+  return la + lb;
 }
 
 // One run of key tiles for one set of row tiles.
@@ -125,23 +242,18 @@ struct PartSeg {
   int slot;            // partial result
 };
 
-// First (item, tile) unit of prefix CTA c, of `units` in all.
-__host__ __device__ __forceinline__ long long part_begin(long long units, int ctas, int c) {
-  return units * c / ctas;
-}
-
 template <int NT, int KT>
 __device__ __forceinline__ bool part_segment(const PartParams& p, int k, PartSeg& s) {
   if (static_cast<int>(blockIdx.x) < p.prefix_ctas) {
-    const long long units = static_cast<long long>(p.prefix_items) * p.prefix_tiles;
-    const long long u0 = part_begin(units, p.prefix_ctas, blockIdx.x);
-    const long long u1 = part_begin(units, p.prefix_ctas, blockIdx.x + 1);
-    const int item0 = static_cast<int>(u0 / p.prefix_tiles);
-    const int item = item0 + k;
-    const long long a = max(u0, static_cast<long long>(item) * p.prefix_tiles);
-    const long long e = min(u1, static_cast<long long>(item + 1) * p.prefix_tiles);
-    if (a >= e || k >= p.max_segs) return false;
-    const int t0 = static_cast<int>(a - static_cast<long long>(item) * p.prefix_tiles);
+    // CTA c has the (item, tile) units [c * run, (c + 1) * run)
+    const unsigned u0 = blockIdx.x * p.prefix_run;
+    const unsigned u1 = min(u0 + p.prefix_run,
+                            static_cast<unsigned>(p.prefix_items) * p.prefix_tiles);
+    const unsigned item = u0 / p.prefix_tiles + k;
+    const unsigned first = item * p.prefix_tiles;
+    const unsigned a = max(u0, first), e = min(u1, first + p.prefix_tiles);
+    if (first >= u1 || a >= e) return false;
+    const int t0 = static_cast<int>(a - first);
     s.n_tiles = static_cast<int>(e - a);
     s.h = item / p.row_groups;
     s.tok0 = (item - s.h * p.row_groups) * NT * p.tpt;
@@ -171,7 +283,7 @@ __device__ __forceinline__ bool part_segment(const PartParams& p, int k, PartSeg
 }
 
 template <int D, int NT, int KT>
-__global__ void __launch_bounds__(64 + NT * 128, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(PartCfg<D, NT, KT>::kThreads, NT == 1 ? 2 : 1)
 attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const PartParams p) {
   using C = PartCfg<D, NT, KT>;
@@ -189,11 +301,13 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   uint64_t* empty = bars + 8;        // [NS] its last MMA has run
   uint64_t* q_full = bars + 16;
   uint64_t* q_empty = bars + 17;     // the segment's last S has run
-  uint64_t* s_full = bars + 18;      // [NT] S of a tile is there (and P V of the one before)
-  uint64_t* p_full = bars + 20;      // [NT] P of a tile is written
+  // S buffer: row tile i (NT = 2), or key tile % 2 (NT = 1)
+  uint64_t* s_full = bars + 18;      // [2] S of a tile is there
+  uint64_t* p_full = bars + 20;      // [2] P of a tile is written
   uint64_t* o_full = bars + 22;      // [NT] the segment's last P V has run
   uint64_t* o_free = bars + 24;      // [NT] O has been read
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
+  uint64_t* pv_done = bars + 26;     // NT = 1: P V of a tile has run
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 27);
   auto ring = [&](int s) { return smem + C::kOffRing + s * C::kTileBytes; };
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -202,12 +316,13 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_free[i], 4);
     }
+    mbar_init(pv_done, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -218,8 +333,11 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   cta_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  auto col_s = [&](int i) { return tmem + i * KT; };
-  auto col_o = [&](int i) { return tmem + NT * KT + i * D; };
+  auto col_s = [&](int buf) { return tmem + buf * KT; };
+  auto col_o = [&](int i) { return tmem + 2 * KT + i * D; };
+  // phase of an S buffer's barriers for the CTA's n-th key tile
+  auto s_buf = [&](int i, unsigned n) { return NT == 2 ? i : static_cast<int>(n & 1); };
+  auto s_phase = [&](unsigned n) { return (NT == 2 ? n : n >> 1) & 1u; };
   // The ring holds K_0, then K_(t+1), V_t for each t: the order of use.
   // K_t is tile 2t - 1 of its segment (K_0: 0), V_t tile 2t + 2 (the last: 2t + 1).
 
@@ -293,67 +411,92 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     if (lane == 0) {
       constexpr uint32_t id_s = part_idesc(128, KT, false);
       constexpr uint32_t id_o = part_idesc(128, D, true);
-      unsigned seq = 0;
-      unsigned tiles = 0;      // key tiles done before this segment
+      const uint64_t dq = umma_desc_sw128(smem_u32(smem));
+      const uint64_t dk = umma_desc_sw128(smem_u32(ring(0)));
+      const uint64_t dv = umma_desc_sw128_mn(smem_u32(ring(0)), KT * 128, 1024);
+      const uint32_t q_lo = static_cast<uint32_t>(dq), q_hi = static_cast<uint32_t>(dq >> 32);
+      const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
+      const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
+      constexpr uint32_t kSlot = C::kTileBytes >> 4;     // addresses count 16 bytes
+      unsigned tiles = 0;                 // key tiles done before this segment
+      unsigned slot = 0, wraps = 0;       // of the next ring tile
       bool ok = true;
-      auto mma_s = [&](int i, int s) {
+      auto advance = [&]() {
+        if (++slot == NS) {
+          slot = 0;
+          ++wraps;
+        }
+      };
+      auto mma_s = [&](int i, int buf, uint32_t k_at) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const int hf = kk >> 2, w = kk & 3;
-          umma_f16kind(col_s(i),
-                       umma_desc_sw128(smem_u32(smem + (i * kHalves + hf) * 128 * 128 + w * 32)),
-                       umma_desc_sw128(smem_u32(ring(s) + hf * KT * 128 + w * 32)), id_s,
-                       kk > 0 ? 1u : 0u);
+          const uint32_t qa = q_lo + (i * kHalves + hf) * (128 * 128 / 16) + w * 2;
+          const uint32_t ka = k_at + hf * (KT * 128 / 16) + w * 2;
+          if (kk == 0) part_mma_ss<false>(col_s(buf), qa, q_hi, ka, k_hi, id_s);
+          else part_mma_ss<true>(col_s(buf), qa, q_hi, ka, k_hi, id_s);
         }
-        umma_commit(&s_full[i]);
+        umma_commit(&s_full[buf]);
       };
-      auto landed = [&](unsigned n) { return mbar_wait(&full[n % NS], (n / NS) & 1, p.err); };
       for (int k = 0; ok && part_segment<NT, KT>(p, k, seg); ++k) {
-        ok = mbar_wait(q_full, k & 1, p.err) && landed(seq);
+        const int n_tiles = seg.n_tiles;
+        ok = mbar_wait(q_full, k & 1, p.err) && mbar_wait(&full[slot], wraps & 1, p.err);
         if (!ok) break;
         tc_fence_after();
-        for (int i = 0; i < NT; ++i) mma_s(i, seq % NS);
-        umma_commit(&empty[seq % NS]);
-        if (seg.n_tiles == 1) umma_commit(q_empty);
-        ++seq;
-        for (int t = 0; ok && t < seg.n_tiles; ++t) {
-          const bool more = t + 1 < seg.n_tiles;
-          const unsigned kq = seq, vq = more ? seq + 1 : seq;
-          for (int i = 0; ok && i < NT; ++i) {
-            ok = mbar_wait(&p_full[i], (tiles + t) & 1, p.err);
-            if (ok && i == 0) ok = landed(vq);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) mma_s(i, s_buf(i, tiles), k_lo + slot * kSlot);
+        umma_commit(&empty[slot]);
+        if (n_tiles == 1) umma_commit(q_empty);
+        advance();
+        for (int t = 0; ok && t < n_tiles; ++t) {
+          const bool more = t + 1 < n_tiles;
+          const unsigned n = tiles + t, kslot = slot, kwraps = wraps;
+          // K of the next tile lies before V of this one in the ring
+          if (more) advance();
+          if (NT == 1 && more) {
+            // the other S buffer's P was read by the P V issued before
+            ok = mbar_wait(&full[kslot], kwraps & 1, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            mma_s(0, s_buf(0, n + 1), k_lo + kslot * kSlot);
+            umma_commit(&empty[kslot]);
+            if (t + 2 == n_tiles) umma_commit(q_empty);
+          }
+          const uint32_t v_at = v_lo + slot * kSlot, k_at = k_lo + kslot * kSlot;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const int buf = s_buf(i, n);
+            if (i == 0) {
+              ok = mbar_wait(&full[slot], wraps & 1, p.err);
+              if (NT == 2 && more && ok) ok = mbar_wait(&full[kslot], kwraps & 1, p.err);
+            }
             // the first P V of a segment overwrites O: the last one's must be read
             if (ok && t == 0) ok = mbar_wait(&o_free[i], (k & 1) ^ 1u, p.err);
+            if (ok) ok = mbar_wait(&p_full[buf], s_phase(n), p.err);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk)
-              part_mma_ts(col_o(i), col_s(i) + kk * 8,
-                          umma_desc_sw128_mn(smem_u32(ring(vq % NS) + kk * 16 * 128), KT * 128,
-                                             1024),
-                          id_o, (t > 0 || kk > 0) ? 1u : 0u);
+              part_mma_ts(col_o(i), col_s(buf) + kk * 8, v_at + kk * (16 * 128 / 16), v_hi, id_o,
+                          kk > 0 || t > 0 ? 1u : 0u);
+            if (NT == 1) umma_commit(pv_done);
             if (!more) umma_commit(&o_full[i]);
-            if (more) {
-              if (i == 0) {
-                ok = landed(kq);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              mma_s(i, kq % NS);
-            }
+            if (NT == 2 && more) mma_s(i, buf, k_at);
           }
           if (!ok) break;
-          if (more) umma_commit(&empty[kq % NS]);
-          umma_commit(&empty[vq % NS]);
-          if (t + 2 == seg.n_tiles) umma_commit(q_empty);
-          seq = vq + 1;
+          if (NT == 2 && more) {
+            umma_commit(&empty[kslot]);
+            if (t + 2 == n_tiles) umma_commit(q_empty);
+          }
+          umma_commit(&empty[slot]);
+          advance();
         }
-        tiles += seg.n_tiles;
+        tiles += n_tiles;
       }
     }
-  } else {
+  } else if (warp >= 2) {
     // ------------------------------------------------------------ softmax
-    const int i = (warp - 2) >> 2;                   // row tile
+    const int i = (warp - 2) >> 2;           // row tile
     const int sp = warp & 3;                         // tensor-memory sub-partition
     const int r = 32 * sp + lane;                    // row of the tile
     const uint32_t lanes = static_cast<uint32_t>(32 * sp) << 16;
@@ -374,63 +517,75 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                                          static_cast<long long>(seg.key1)));
         }
       }
+      // a warp without rows only keeps step: its P and O rows are never stored
+      const bool rows = __any_sync(0xffffffffu, limit > seg.key0);
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < seg.n_tiles; ++t) {
-        if (ok) ok = mbar_wait(&s_full[i], (tiles + t) & 1, p.err);
+        const unsigned n = tiles + t;
+        const int buf = s_buf(i, n);
+        if (ok) ok = mbar_wait(&s_full[buf], s_phase(n), p.err);
         tc_fence_after();
-        float x[KT];
+        if (rows) {
+          const int left = limit - (seg.key0 + t * KT);    // keys of the tile that the row sees
+          const bool masked = __any_sync(0xffffffffu, left < KT);
+          const uint32_t s_at = col_s(buf) + lanes;
+          float mx;
+          {
+            // S is read twice, for the maximum and for P: the second reading costs
+            // less than the registers that a row of it would hold meanwhile
+            float x[KT];
 #pragma unroll
-        for (int c = 0; c < KT / 32; ++c) tmem_ld_32x32b_x32(col_s(i) + lanes + c * 32, x + c * 32);
-        tmem_ld_wait();
-        const int left = limit - (seg.key0 + t * KT);    // keys of the tile that the row sees
-        if (__any_sync(0xffffffffu, left < KT)) {
+            for (int c = 0; c < KT / 32; ++c) tmem_ld_32x32b_x32(s_at + c * 32, x + c * 32);
+            tmem_ld_wait();
+            if (masked) {
 #pragma unroll
-          for (int c = 0; c < KT; ++c)
-            if (c >= left) x[c] = -INFINITY;
-        }
-        float mx = x[0];
+              for (int c = 0; c < KT; ++c)
+                if (c >= left) x[c] = -INFINITY;
+            }
+            float mx4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 1; c < KT; ++c) mx = fmaxf(mx, x[c]);
-        mx *= scale;
-        // The reference is the first maximum that the row meets; it is raised
-        // only when a score outgrows it by the headroom (2^32 keeps P, l and O
-        // far inside their types), so O is rarely rescaled.
-        if (__any_sync(0xffffffffu, mx > m + kPartHeadroom)) {
-          const float up = mx > m + kPartHeadroom ? mx : m;
-          const float a = m == -INFINITY ? 0.f : part_ex2(m - up);
-          const bool has = __any_sync(0xffffffffu, m != -INFINITY);
-          m = up;
-          l *= a;
-          if (has && t > 0) {     // P V of the tile before has run: s_full came after it
+            for (int c = 4; c + 8 <= KT; c += 8) {
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float o[32];
-              tmem_ld_32x32b_x32(col_o(i) + lanes + c * 32, o);
-              tmem_ld_wait();
+              for (int e = 0; e < 4; ++e) mx4[e] = part_max3(mx4[e], x[c + e], x[c + 4 + e]);
+            }
+            mx = part_max3(part_max3(mx4[0], mx4[1], x[KT - 4]),
+                           part_max3(mx4[2], mx4[3], x[KT - 3]),
+                           part_max3(x[KT - 2], x[KT - 1], x[KT - 1])) * scale;
+          }
+          // The reference is the first maximum that the row meets; it is raised
+          // only when a score outgrows it by the headroom (2^32 keeps P, l and O
+          // far inside their types), so O is rarely rescaled.
+          if (__any_sync(0xffffffffu, mx > m + kPartHeadroom)) {
+            const float up = mx > m + kPartHeadroom ? mx : m;
+            const float a = m == -INFINITY ? 0.f : part_ex2(m - up);
+            const bool has = __any_sync(0xffffffffu, m != -INFINITY);
+            m = up;
+            l *= a;
+            if (has && t > 0) {
+              // P V of the tile before must have run: with NT = 2 s_full came after it
+              if (NT == 1) {
+                if (ok) ok = mbar_wait(pv_done, (n - 1) & 1u, p.err);
+                tc_fence_after();
+              }
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= a;
-              uint32_t w[32];
+              for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                tmem_ld_32x32b_x32(col_o(i) + lanes + c * 32, o);
+                tmem_ld_wait();
+                uint32_t w[32];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e]);
-              part_st_x32(col_o(i) + lanes + c * 32, w);
+                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * a);
+                part_st_x32(col_o(i) + lanes + c * 32, w);
+              }
             }
           }
-        }
-        const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int c = 0; c < KT / 64; ++c) {
-          uint32_t w[32];
-          float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float a = part_ex2(fmaf(x[c * 64 + 2 * e], scale, -ref));
-            const float b = part_ex2(fmaf(x[c * 64 + 2 * e + 1], scale, -ref));
-            l0 += a;
-            l1 += b;
-            w[e] = pack_bf16x2(a, b);
-          }
-          l += l0 + l1;
-          part_st_x32(col_s(i) + lanes + c * 32, w);
+          const float ref = m == -INFINITY ? 0.f : m;
+          // Of an unmasked tile a quarter of the exponentials goes to the FMA pipes:
+          // 16 a cycle of the special-function pipe, for 128 x 128 of them, is as
+          // long as the tile's two products.  (A NaN, too, takes the other way.)
+          l += masked || __any_sync(0xffffffffu, mx != mx)
+                   ? part_weights<KT, false>(s_at, scale, ref, left)
+                   : part_weights<KT, true>(s_at, scale, ref, left);
         }
         if (NT == 1 && sp == 0 && t + 1 == seg.n_tiles && (seg.key1 & 15)) {
           // rows of V past the last key of its page may hold anything (NaN too):
@@ -449,7 +604,7 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[i]);
+        if (lane == 0) mbar_arrive(&p_full[buf]);
       }
       // the part: O, and (m, l) of the row
       if (ok) ok = mbar_wait(&o_full[i], k & 1, p.err);
@@ -457,10 +612,11 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const bool own = seg.b >= 0;
       float* dst = own ? p.own_o + (static_cast<size_t>(seg.slot) * p.R + r) * D
                        : p.prefix_o + ((static_cast<size_t>(seg.slot) * NT + i) * 128 + r) * D;
-      const bool store = ok && l != 0.f &&   // a NaN is a result
+      const bool store = ok && rows && l != 0.f &&   // a NaN is a result
                           (!own || r < p.R);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
+        if (!rows) break;
         float o[32];
         tmem_ld_32x32b_x32(col_o(i) + lanes + c * 32, o);
         tmem_ld_wait();
@@ -491,8 +647,9 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
 }
 
-// One warp joins the parts of one (token, query head); prefix_nt, prefix_kt: the
-// row tiles and keys a tile of the kernel that ran the prefix.
+// One warp joins the parts of one (token, query head); prefix_nt: the row tiles
+// of the kernel that ran the prefix.  The lanes read the parts' (m, l) side by
+// side, then every part's row of O with its weight known, so the loads overlap.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int prefix_nt,
                                                         f16* __restrict__ out) {
@@ -506,42 +663,68 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int 
   const int b = tok / p.q_len, j = tok - b * p.q_len;
   const int seq = p.seq_lens[b];
   if (seq < 0) return;                       // a padding request keeps its rows
-  float M = -INFINITY, l = 0.f, acc[kPer];
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  auto add = [&](const float2 ml, const float* o) {
-    if (ml.y == 0.f) return;               // the row saw no key of this part
-    const float top = fmaxf(M, ml.x);
-    const float keep = M == -INFINITY ? 0.f : part_ex2(M - top), w = part_ex2(ml.x - top);
-    M = top;
-    l = l * keep + ml.y * w;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * keep + o[lane * kPer + e] * w;
-  };
+  // parts: the prefix CTAs c0 .. that ran this item, then the own splits
+  unsigned c0 = 0, item = 0;
+  int n_prefix = 0, in_item = 0;
   if (p.prefix_ctas > 0) {
     const int tile = tok / p.tpt, rg = tile / prefix_nt;
-    const int item = h * p.row_groups + rg;
-    const int row = (tok - tile * p.tpt) * p.G + g;
-    const long long units = static_cast<long long>(p.prefix_items) * p.prefix_tiles;
-    const long long a = static_cast<long long>(item) * p.prefix_tiles, e = a + p.prefix_tiles;
-    int c = static_cast<int>(a * p.prefix_ctas / units);
-    while (c + 1 < p.prefix_ctas && part_begin(units, p.prefix_ctas, c + 1) <= a) ++c;
-    while (c > 0 && part_begin(units, p.prefix_ctas, c) > a) --c;
-    for (; c < p.prefix_ctas && part_begin(units, p.prefix_ctas, c) < e; ++c) {
-      const long long u0 = part_begin(units, p.prefix_ctas, c);
-      if (part_begin(units, p.prefix_ctas, c + 1) <= max(a, u0)) continue;   // nothing dealt
-      const int k = item - static_cast<int>(u0 / p.prefix_tiles);
-      const size_t at = ((static_cast<size_t>(c) * p.max_segs + k) * prefix_nt +
-                         (tile - rg * prefix_nt)) * 128 + row;
-      add(p.prefix_ml[at], p.prefix_o + at * D);
-    }
+    item = h * p.row_groups + rg;
+    in_item = (tile - rg * prefix_nt) * 128 + (tok - tile * p.tpt) * p.G + g;
+    c0 = item * p.prefix_tiles / p.prefix_run;
+    n_prefix = ((item + 1) * p.prefix_tiles - 1) / p.prefix_run - c0 + 1;
   }
   const long long own = static_cast<long long>(seq) + p.q_len - p.prefix_keys;
   if (own > static_cast<long long>(p.W) * 16 - p.prefix_keys && lane == 0 && j == 0 && head == 0)
     raise_error(p.err, DFLASH_DEVERR_TABLE);
-  for (int s = 0; s < p.max_splits && static_cast<long long>(s) * p.chunk_keys < own; ++s) {
-    const size_t at = ((static_cast<size_t>(s) * p.B + b) * p.Hkv + h) * p.R + j * p.G + g;
-    add(p.own_ml[at], p.own_o + at * D);
+  const int n_own = own <= 0 ? 0
+                             : static_cast<int>(min(static_cast<long long>(p.max_splits),
+                                                    (own + p.chunk_keys - 1) / p.chunk_keys));
+  const int parts = n_prefix + n_own;
+  float M = -INFINITY, l = 0.f, acc[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  for (int q0 = 0; q0 < parts; q0 += 32) {
+    const int q = q0 + lane;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    const float* o = nullptr;
+    if (q < n_prefix) {
+      const unsigned c = c0 + q;
+      const unsigned k = item - c * p.prefix_run / p.prefix_tiles;
+      const size_t at =
+          (static_cast<size_t>(c) * p.max_segs + k) * prefix_nt * 128 + in_item;
+      ml = p.prefix_ml[at];
+      o = p.prefix_o + at * D;
+    } else if (q < parts) {
+      const size_t at =
+          ((static_cast<size_t>(q - n_prefix) * p.B + b) * p.Hkv + h) * p.R + j * p.G + g;
+      ml = p.own_ml[at];
+      o = p.own_o + at * D;
+    }
+    if (ml.y == 0.f) ml.x = -INFINITY;       // the row saw no key of this part
+    float top = fmaxf(M, ml.x);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    const float keep = M == -INFINITY ? 0.f : part_ex2(M - top);
+    // (a part whose l is NaN keeps its weight whatever its reference)
+    const float w = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : part_ex2(ml.x - top);
+    M = top;
+    float lw = ml.y * w;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, s);
+    l = l * keep + lw;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] *= keep;
+    const int n = min(32, parts - q0);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float ws = __shfl_sync(0xffffffffu, w, s);
+      const float* os = reinterpret_cast<const float*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), s));
+      if (ws != 0.f) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] += os[lane * kPer + e] * ws;
+      }
+    }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
   f16* o = out + static_cast<size_t>(unit) * D + lane * kPer;
