@@ -52,7 +52,7 @@ struct PrefixPlan {
   int nt = 1, kt = 64;           // the prefix's kernel
   int tpt = 0, row_groups = 0, items = 0, tiles = 0, ctas = 0, max_segs = 0;
   int64_t run = 1;               // (item, tile) units of a CTA
-  bool too_many = false;         // units past 31 bits
+  bool too_many = false;         // units, or own items, past 31 bits
   int chunk = 0, splits = 0, R = 0;
   size_t off_ml = 0, off_own = 0, off_own_ml = 0, total = 0;
 };
@@ -85,6 +85,7 @@ PrefixPlan plan_prefix(const dflash_handle* h, int B, int q_len, int W, int pref
     chunk = std::max(128, std::min(8192, (chunk + 63) / 64 * 64));
     p.chunk = chunk;
     p.splits = cdiv(own_keys, chunk);
+    p.too_many |= static_cast<int64_t>(p.splits) * B * Hkv > INT32_MAX / 2;
   }
   const size_t pr = static_cast<size_t>(p.ctas) * p.max_segs * p.nt * 128;
   const size_t ow = static_cast<size_t>(p.splits) * B * Hkv * p.R;
@@ -137,12 +138,15 @@ dflash_status run_prefix(dflash_handle* h, const PrefixPlan& pl, PartParams p, c
     s = launch_part<D, 2, 128>(h, tq, tk, tv, p, pl.ctas, st);
     own.prefix_ctas = 0;
   }
-  const int64_t ctas = own.prefix_ctas + static_cast<int64_t>(pl.splits) * p.B * p.Hkv;
+  // the own keys' CTAs stay and take one item after another, so that the loads of
+  // the next overlap the end of the last
+  const int64_t ctas = own.prefix_ctas + std::min<int64_t>(
+      static_cast<int64_t>(pl.splits) * p.B * p.Hkv, 2 * h->num_sms);
   if (s == DFLASH_OK && ctas > 0) s = launch_part<D, 1, 64>(h, tq, tk, tv, own, ctas, st);
   if (s != DFLASH_OK) return s;
   LaunchScope scope(h, DFLASH_KERNEL_PREFIX_COMBINE, st);
   launch_k(h->pdl, attn_join_kernel<D>, dim3(static_cast<unsigned>(
-               (static_cast<int64_t>(p.n_tok) * p.Hq + 7) / 8)), dim3(256), 0, st, p, pl.nt, o);
+               (static_cast<int64_t>(p.n_tok) * p.Hkv + 7) / 8)), dim3(256), 0, st, p, pl.nt, o);
   return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 

@@ -22,6 +22,13 @@
 // NT = 2: the issue order PV_0(t) S_0(t+1) PV_1(t) S_1(t+1) keeps the tensor cores
 // on one row tile while the other one's softmax runs.  NT = 1: S has two buffers,
 // S(t+1) is issued before P V(t), and a second CTA on the SM fills the rest.
+//
+// Measured at 128 requests x 10 rows over 16384 shared keys (NT = 2): a pair of
+// row tiles takes 3400 cycles a key tile, 2200 of them products (2048 at the full
+// rate); what is left is the chain S, softmax (1640), P V of a row tile.  Tried
+// and slower: an issuer for each row tile (448 us against 347), eight softmax
+// warps a row tile (357), a quarter or half of the exponentials as polynomials on
+// the FMA pipes (347, 373).
 //   NT = 2, KT = 128: one CTA an SM, 4 D x 128 flops per byte read, for many rows
 //   NT = 1, KT = 64:  two CTAs an SM, for one request's rows
 #pragma once
@@ -47,7 +54,7 @@ struct PartParams {
   int max_segs;
   float* prefix_o;     // [prefix_ctas][max_segs][NT][128][D]
   float2* prefix_ml;   // [prefix_ctas][max_segs][NT][128]
-  // own keys: one CTA per (split, request, kv head)
+  // own keys: (split, request, kv head) items, dealt to the other CTAs in turn
   int chunk_keys, max_splits, R;          // R = q_len * G
   float* own_o;        // [max_splits][B][Hkv][R][D]
   float2* own_ml;      // [max_splits][B][Hkv][R]
@@ -71,6 +78,7 @@ struct PartCfg {
   static constexpr int kThreads = 64 + NT * 128;
   static constexpr int kUsed = 2 * KT + NT * D;            // S twice, O
   static constexpr int kCols = kUsed > 256 ? 512 : kUsed > 128 ? 256 : 128;
+  static_assert(kSmem <= 232448, "shared memory");
   static_assert(NS >= 3, "ring");
   static_assert(kCols * kCtas <= 512, "tensor memory");
 };
@@ -164,40 +172,16 @@ __device__ __forceinline__ f32x2 part_add2(f32x2 a, f32x2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ float part_max3(float a, float b, float c) {   // a NaN stays
+__device__ __forceinline__ float part_max3(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-constexpr float kExpC0 = 0.999928074f, kExpC1 = 0.693260985f, kExpC2 = 0.242611122f,
-                kExpC3 = 0.0551716691f;
-// 2^y of a pair on the FMA pipes, y <= 2^6: 2^y = 2^n 2^f, n = rint(y), |f| <= 1/2,
-// 2^f by the cubic of least relative error there (7.5e-5, found by a Remez exchange;
-// P is rounded to bf16, 4e-3, next).  Below -126 it stays at 2^-126.
-__device__ __forceinline__ void part_exp2_pair(f32x2 y, float& a, float& b) {
-  float ya, yb;
-  part_unpack(y, ya, yb);
-  y = part_pack(fmaxf(ya, -126.f), fmaxf(yb, -126.f));
-  const f32x2 magic = part_pack(12582912.f, 12582912.f);   // 1.5 2^23
-  const f32x2 unmagic = part_pack(-12582912.f, -12582912.f);
-  const f32x2 n = part_add2(y, magic);
-  const f32x2 whole = part_add2(n, unmagic);
-  const f32x2 f = part_fma2(whole, part_pack(-1.f, -1.f), y);
-  f32x2 p = part_pack(kExpC3, kExpC3);
-  p = part_fma2(p, f, part_pack(kExpC2, kExpC2));
-  p = part_fma2(p, f, part_pack(kExpC1, kExpC1));
-  p = part_fma2(p, f, part_pack(kExpC0, kExpC0));
-  float na, nb, pa, pb;
-  part_unpack(n, na, nb);
-  part_unpack(p, pa, pb);
-  a = __int_as_float(__float_as_int(pa) + (__float_as_int(na) << 23));
-  b = __int_as_float(__float_as_int(pb) + (__float_as_int(nb) << 23));
-}
 
-// P = 2^(s scale - ref) in the place of a row's KT scores, as bf16 pairs; returns
-// the row's sum.  In chunks of 32 scores: chunk c is read from columns 32 c ..
+// P = 2^(s scale - ref) in the place of KT of a row's scores, as bf16 pairs; returns
+// their sum.  In chunks of 32 scores: chunk c is read from columns 32 c ..
 // and written to columns 16 c .., never ahead of what is still to be read.
-template <int KT, bool FAST>
+template <int KT, bool MASKED>
 __device__ __forceinline__ float part_weights(uint32_t s_at, float scale, float ref, int left) {
   const f32x2 sc2 = part_pack(scale, scale), nr2 = part_pack(-ref, -ref);
   f32x2 l2[2] = {part_pack(0.f, 0.f), part_pack(0.f, 0.f)};
@@ -211,18 +195,14 @@ __device__ __forceinline__ float part_weights(uint32_t s_at, float scale, float 
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       float a = x[c & 1][2 * e], b = x[c & 1][2 * e + 1];
-      if (!FAST) {
+      if (MASKED) {
         if (c * 32 + 2 * e >= left) a = -INFINITY;
         if (c * 32 + 2 * e + 1 >= left) b = -INFINITY;
       }
       const f32x2 y = part_fma2(part_pack(a, b), sc2, nr2);
-      if (FAST && (e & 3) == 3) {
-        part_exp2_pair(y, a, b);
-      } else {
-        part_unpack(y, a, b);
-        a = part_ex2(a);
-        b = part_ex2(b);
-      }
+      part_unpack(y, a, b);
+      a = part_ex2(a);
+      b = part_ex2(b);
       l2[e & 1] = part_add2(l2[e & 1], part_pack(a, b));
       w[e] = pack_bf16x2(a, b);
     }
@@ -242,45 +222,55 @@ struct PartSeg {
   int slot;            // partial result
 };
 
+// The CTA's segments in turn; every role of the CTA walks them alike.
 template <int NT, int KT>
-__device__ __forceinline__ bool part_segment(const PartParams& p, int k, PartSeg& s) {
-  if (static_cast<int>(blockIdx.x) < p.prefix_ctas) {
-    // CTA c has the (item, tile) units [c * run, (c + 1) * run)
-    const unsigned u0 = blockIdx.x * p.prefix_run;
-    const unsigned u1 = min(u0 + p.prefix_run,
-                            static_cast<unsigned>(p.prefix_items) * p.prefix_tiles);
-    const unsigned item = u0 / p.prefix_tiles + k;
-    const unsigned first = item * p.prefix_tiles;
-    const unsigned a = max(u0, first), e = min(u1, first + p.prefix_tiles);
-    if (first >= u1 || a >= e) return false;
-    const int t0 = static_cast<int>(a - first);
-    s.n_tiles = static_cast<int>(e - a);
-    s.h = item / p.row_groups;
-    s.tok0 = (item - s.h * p.row_groups) * NT * p.tpt;
-    s.b = -1;
-    s.key0 = t0 * KT;
-    s.key1 = min(p.prefix_keys, (t0 + s.n_tiles) * KT);
-    s.slot = blockIdx.x * p.max_segs + k;
-    return true;
+struct PartWalk {
+  int next = 0;       // next one to look at
+  __device__ __forceinline__ bool step(const PartParams& p, PartSeg& s) {
+    if (static_cast<int>(blockIdx.x) < p.prefix_ctas) {
+      // CTA c has the (item, tile) units [c * run, (c + 1) * run)
+      const unsigned u0 = blockIdx.x * p.prefix_run;
+      const unsigned u1 = min(u0 + p.prefix_run,
+                              static_cast<unsigned>(p.prefix_items) * p.prefix_tiles);
+      const unsigned item = u0 / p.prefix_tiles + next;
+      const unsigned first = item * p.prefix_tiles;
+      const unsigned a = max(u0, first), e = min(u1, first + p.prefix_tiles);
+      if (first >= u1 || a >= e) return false;
+      const int t0 = static_cast<int>(a - first);
+      s.n_tiles = static_cast<int>(e - a);
+      s.h = item / p.row_groups;
+      s.tok0 = (item - s.h * p.row_groups) * NT * p.tpt;
+      s.b = -1;
+      s.key0 = t0 * KT;
+      s.key1 = min(p.prefix_keys, (t0 + s.n_tiles) * KT);
+      s.slot = blockIdx.x * p.max_segs + next;
+      ++next;
+      return true;
+    }
+    // own keys: items (split, request, kv head), the kv head fastest, a grid apart
+    const int stride = static_cast<int>(gridDim.x) - p.prefix_ctas;
+    const int total = p.max_splits * p.B * p.Hkv;
+    for (int i = static_cast<int>(blockIdx.x) - p.prefix_ctas + next * stride; i < total;
+         i += stride) {
+      ++next;
+      const int rest = i / p.Hkv, split = rest / p.B;
+      s.b = rest - split * p.B;
+      const int seq = p.seq_lens[s.b];
+      s.key0 = p.prefix_keys + split * p.chunk_keys;
+      // 64-bit: seq may be anything
+      s.key1 = seq < 0 ? 0
+                       : static_cast<int>(min(static_cast<long long>(seq) + p.q_len,
+                                              static_cast<long long>(s.key0) + p.chunk_keys));
+      if (s.key0 >= s.key1) continue;
+      s.h = i - rest * p.Hkv;
+      s.n_tiles = (s.key1 - s.key0 + KT - 1) / KT;
+      s.tok0 = s.b * p.q_len;
+      s.slot = i;
+      return true;
+    }
+    return false;
   }
-  if (k > 0) return false;
-  int i = static_cast<int>(blockIdx.x) - p.prefix_ctas;
-  s.h = i % p.Hkv;
-  i /= p.Hkv;
-  s.b = i % p.B;
-  const int split = i / p.B;
-  const int seq = p.seq_lens[s.b];
-  s.key0 = p.prefix_keys + split * p.chunk_keys;
-  // 64-bit: seq may be anything
-  s.key1 = seq < 0 ? 0
-                   : static_cast<int>(min(static_cast<long long>(seq) + p.q_len,
-                                          static_cast<long long>(s.key0) + p.chunk_keys));
-  if (s.key0 >= s.key1) return false;
-  s.n_tiles = (s.key1 - s.key0 + KT - 1) / KT;
-  s.tok0 = s.b * p.q_len;
-  s.slot = (split * p.B + s.b) * p.Hkv + s.h;
-  return true;
-}
+};
 
 template <int D, int NT, int KT>
 __global__ void __launch_bounds__(PartCfg<D, NT, KT>::kThreads, NT == 1 ? 2 : 1)
@@ -291,7 +281,11 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   pdl_trigger();
   pdl_wait();
   PartSeg seg;
-  if (!part_segment<NT, KT>(p, 0, seg)) return;   // the same for the whole CTA
+  {
+    PartWalk<NT, KT> first;
+    if (!first.step(p, seg)) return;   // the same for the whole CTA
+  }
+  PartWalk<NT, KT> walk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   extern __shared__ uint8_t part_smem[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(part_smem) + 1023) &
@@ -348,7 +342,7 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const bool loads = lane < kPages * kHalves;
     unsigned seq = 0;      // ring tiles issued
     bool ok = true;
-    for (int k = 0; ok && part_segment<NT, KT>(p, k, seg); ++k) {
+    for (int k = 0; ok && walk.step(p, seg); ++k) {
       if (lane == 0) {
         ok = mbar_wait(q_empty, (k & 1) ^ 1u, p.err);
         if (ok) {
@@ -438,7 +432,7 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
         umma_commit(&s_full[buf]);
       };
-      for (int k = 0; ok && part_segment<NT, KT>(p, k, seg); ++k) {
+      for (int k = 0; ok && walk.step(p, seg); ++k) {
         const int n_tiles = seg.n_tiles;
         ok = mbar_wait(q_full, k & 1, p.err) && mbar_wait(&full[slot], wraps & 1, p.err);
         if (!ok) break;
@@ -450,26 +444,24 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         advance();
         for (int t = 0; ok && t < n_tiles; ++t) {
           const bool more = t + 1 < n_tiles;
-          const unsigned n = tiles + t, kslot = slot, kwraps = wraps;
+          const unsigned n = tiles + t, kslot = slot;
           // K of the next tile lies before V of this one in the ring
-          if (more) advance();
-          if (NT == 1 && more) {
-            // the other S buffer's P was read by the P V issued before
-            ok = mbar_wait(&full[kslot], kwraps & 1, p.err);
-            if (!ok) break;
-            tc_fence_after();
-            mma_s(0, s_buf(0, n + 1), k_lo + kslot * kSlot);
-            umma_commit(&empty[kslot]);
-            if (t + 2 == n_tiles) umma_commit(q_empty);
+          if (more) {
+            ok = mbar_wait(&full[kslot], wraps & 1, p.err);
+            advance();
+            if (NT == 1 && ok) {
+              // the other S buffer's P was read by the P V issued before
+              tc_fence_after();
+              mma_s(0, s_buf(0, n + 1), k_lo + kslot * kSlot);
+              umma_commit(&empty[kslot]);
+              if (t + 2 == n_tiles) umma_commit(q_empty);
+            }
           }
-          const uint32_t v_at = v_lo + slot * kSlot, k_at = k_lo + kslot * kSlot;
+          if (ok) ok = mbar_wait(&full[slot], wraps & 1, p.err);
+          const uint32_t v_at = v_lo + slot * kSlot;
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             const int buf = s_buf(i, n);
-            if (i == 0) {
-              ok = mbar_wait(&full[slot], wraps & 1, p.err);
-              if (NT == 2 && more && ok) ok = mbar_wait(&full[kslot], kwraps & 1, p.err);
-            }
             // the first P V of a segment overwrites O: the last one's must be read
             if (ok && t == 0) ok = mbar_wait(&o_free[i], (k & 1) ^ 1u, p.err);
             if (ok) ok = mbar_wait(&p_full[buf], s_phase(n), p.err);
@@ -481,7 +473,7 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                           kk > 0 || t > 0 ? 1u : 0u);
             if (NT == 1) umma_commit(pv_done);
             if (!more) umma_commit(&o_full[i]);
-            if (NT == 2 && more) mma_s(i, buf, k_at);
+            if (NT == 2 && more) mma_s(i, buf, k_lo + kslot * kSlot);
           }
           if (!ok) break;
           if (NT == 2 && more) {
@@ -494,16 +486,16 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         tiles += n_tiles;
       }
     }
-  } else if (warp >= 2) {
+  } else {
     // ------------------------------------------------------------ softmax
-    const int i = (warp - 2) >> 2;           // row tile
+    const int i = (warp - 2) >> 2;                   // row tile
     const int sp = warp & 3;                         // tensor-memory sub-partition
     const int r = 32 * sp + lane;                    // row of the tile
     const uint32_t lanes = static_cast<uint32_t>(32 * sp) << 16;
     const float scale = p.scale_log2;
     unsigned tiles = 0, seq = 0;
     bool ok = true;
-    for (int k = 0; part_segment<NT, KT>(p, k, seg); ++k) {
+    for (int k = 0; walk.step(p, seg); ++k) {
       // keys that this row sees: none if it is no row of this segment
       int limit = 0;
       {
@@ -526,9 +518,9 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (ok) ok = mbar_wait(&s_full[buf], s_phase(n), p.err);
         tc_fence_after();
         if (rows) {
+          const uint32_t s_at = col_s(buf) + lanes;
           const int left = limit - (seg.key0 + t * KT);    // keys of the tile that the row sees
           const bool masked = __any_sync(0xffffffffu, left < KT);
-          const uint32_t s_at = col_s(buf) + lanes;
           float mx;
           {
             // S is read twice, for the maximum and for P: the second reading costs
@@ -550,11 +542,11 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             }
             mx = part_max3(part_max3(mx4[0], mx4[1], x[KT - 4]),
                            part_max3(mx4[2], mx4[3], x[KT - 3]),
-                           part_max3(x[KT - 2], x[KT - 1], x[KT - 1])) * scale;
+                           fmaxf(x[KT - 2], x[KT - 1])) * scale;
           }
-          // The reference is the first maximum that the row meets; it is raised
-          // only when a score outgrows it by the headroom (2^32 keeps P, l and O
-          // far inside their types), so O is rarely rescaled.
+          // The reference is the first maximum that the row meets; it is raised only
+          // when a score outgrows it by the headroom (2^32 keeps P, l and O far inside
+          // their types), so O is rarely rescaled.
           if (__any_sync(0xffffffffu, mx > m + kPartHeadroom)) {
             const float up = mx > m + kPartHeadroom ? mx : m;
             const float a = m == -INFINITY ? 0.f : part_ex2(m - up);
@@ -580,12 +572,8 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          // Of an unmasked tile a quarter of the exponentials goes to the FMA pipes:
-          // 16 a cycle of the special-function pipe, for 128 x 128 of them, is as
-          // long as the tile's two products.  (A NaN, too, takes the other way.)
-          l += masked || __any_sync(0xffffffffu, mx != mx)
-                   ? part_weights<KT, false>(s_at, scale, ref, left)
-                   : part_weights<KT, true>(s_at, scale, ref, left);
+          l += masked ? part_weights<KT, true>(s_at, scale, ref, left)
+                      : part_weights<KT, false>(s_at, scale, ref, left);
         }
         if (NT == 1 && sp == 0 && t + 1 == seg.n_tiles && (seg.key1 & 15)) {
           // rows of V past the last key of its page may hold anything (NaN too):
@@ -613,7 +601,7 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       float* dst = own ? p.own_o + (static_cast<size_t>(seg.slot) * p.R + r) * D
                        : p.prefix_o + ((static_cast<size_t>(seg.slot) * NT + i) * 128 + r) * D;
       const bool store = ok && rows && l != 0.f &&   // a NaN is a result
-                          (!own || r < p.R);
+                         (!own || r < p.R);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         if (!rows) break;
@@ -647,9 +635,10 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
 }
 
-// One warp joins the parts of one (token, query head); prefix_nt: the row tiles
-// of the kernel that ran the prefix.  The lanes read the parts' (m, l) side by
-// side, then every part's row of O with its weight known, so the loads overlap.
+// One warp joins the parts of a token's kv group (G query heads); prefix_nt: the
+// row tiles of the kernel that ran the prefix.  The lanes read the parts' (m, l)
+// side by side, then every part's row of O with its weight known, so that the
+// loads of a head overlap.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int prefix_nt,
                                                         f16* __restrict__ out) {
@@ -657,9 +646,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int 
   pdl_wait();
   constexpr int kPer = D / 32;
   const int unit = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (unit >= p.n_tok * p.Hq) return;
-  const int tok = unit / p.Hq, head = unit - tok * p.Hq;
-  const int h = head / p.G, g = head - h * p.G;
+  if (unit >= p.n_tok * p.Hkv) return;
+  const int tok = unit / p.Hkv, h = unit - tok * p.Hkv;
   const int b = tok / p.q_len, j = tok - b * p.q_len;
   const int seq = p.seq_lens[b];
   if (seq < 0) return;                       // a padding request keeps its rows
@@ -669,68 +657,77 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int 
   if (p.prefix_ctas > 0) {
     const int tile = tok / p.tpt, rg = tile / prefix_nt;
     item = h * p.row_groups + rg;
-    in_item = (tile - rg * prefix_nt) * 128 + (tok - tile * p.tpt) * p.G + g;
+    in_item = (tile - rg * prefix_nt) * 128 + (tok - tile * p.tpt) * p.G;
     c0 = item * p.prefix_tiles / p.prefix_run;
     n_prefix = ((item + 1) * p.prefix_tiles - 1) / p.prefix_run - c0 + 1;
   }
   const long long own = static_cast<long long>(seq) + p.q_len - p.prefix_keys;
-  if (own > static_cast<long long>(p.W) * 16 - p.prefix_keys && lane == 0 && j == 0 && head == 0)
+  if (own > static_cast<long long>(p.W) * 16 - p.prefix_keys && lane == 0 && j == 0 && h == 0)
     raise_error(p.err, DFLASH_DEVERR_TABLE);
   const int n_own = own <= 0 ? 0
                              : static_cast<int>(min(static_cast<long long>(p.max_splits),
                                                     (own + p.chunk_keys - 1) / p.chunk_keys));
   const int parts = n_prefix + n_own;
-  float M = -INFINITY, l = 0.f, acc[kPer];
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  for (int q0 = 0; q0 < parts; q0 += 32) {
-    const int q = q0 + lane;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    const float* o = nullptr;
+  // lane q: where part q's rows of this group are
+  auto at = [&](int q) -> size_t {
     if (q < n_prefix) {
       const unsigned c = c0 + q;
       const unsigned k = item - c * p.prefix_run / p.prefix_tiles;
-      const size_t at =
-          (static_cast<size_t>(c) * p.max_segs + k) * prefix_nt * 128 + in_item;
-      ml = p.prefix_ml[at];
-      o = p.prefix_o + at * D;
-    } else if (q < parts) {
-      const size_t at =
-          ((static_cast<size_t>(q - n_prefix) * p.B + b) * p.Hkv + h) * p.R + j * p.G + g;
-      ml = p.own_ml[at];
-      o = p.own_o + at * D;
+      return (static_cast<size_t>(c) * p.max_segs + k) * prefix_nt * 128 + in_item;
     }
-    if (ml.y == 0.f) ml.x = -INFINITY;       // the row saw no key of this part
-    float top = fmaxf(M, ml.x);
+    return ((static_cast<size_t>(q - n_prefix) * p.B + b) * p.Hkv + h) * p.R + j * p.G;
+  };
+  const size_t first = at(min(lane, max(parts - 1, 0)));
+  f16* dst = out + (static_cast<size_t>(tok) * p.Hq + h * p.G) * D + lane * kPer;
+  for (int g = 0; g < p.G; ++g) {
+    float M = -INFINITY, l = 0.f, acc[kPer];
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    const float keep = M == -INFINITY ? 0.f : part_ex2(M - top);
-    // (a part whose l is NaN keeps its weight whatever its reference)
-    const float w = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : part_ex2(ml.x - top);
-    M = top;
-    float lw = ml.y * w;
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    for (int q0 = 0; q0 < parts; q0 += 32) {
+      const int q = q0 + lane;
+      const size_t mine = (q0 == 0 ? first : q < parts ? at(q) : 0) + g;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      const float* o = nullptr;
+      if (q < parts) {
+        ml = (q < n_prefix ? p.prefix_ml : p.own_ml)[mine];
+        o = (q < n_prefix ? p.prefix_o : p.own_o) + mine * D;
+      }
+      if (ml.y == 0.f) ml.x = -INFINITY;       // the row saw no key of this part
+      float top = fmaxf(M, ml.x);
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, s);
-    l = l * keep + lw;
+      for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+      const float keep = M == -INFINITY ? 0.f : part_ex2(M - top);
+      // (a part whose l is NaN keeps its weight whatever its reference)
+      const float w = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : part_ex2(ml.x - top);
+      M = top;
+      float lw = ml.y * w;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] *= keep;
-    const int n = min(32, parts - q0);
+      for (int s = 16; s > 0; s >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, s);
+      l = l * keep + lw;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] *= keep;
+      const int n = min(32, parts - q0);
 #pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-      const float ws = __shfl_sync(0xffffffffu, w, s);
-      const float* os = reinterpret_cast<const float*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), s));
-      if (ws != 0.f) {
+      for (int s = 0; s < n; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, w, s);
+        const float* os = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), s));
+        if (ws != 0.f) {
+          float v[kPer];
+          if constexpr (kPer == 4)
+            *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(os + lane * 4);
+          else
+            *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(os + lane * 2);
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] += os[lane * kPer + e] * ws;
+          for (int e = 0; e < kPer; ++e) acc[e] += v[e] * ws;
+        }
       }
     }
-  }
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  f16* o = out + static_cast<size_t>(unit) * D + lane * kPer;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int e = 0; e < kPer; e += 2)
-    *reinterpret_cast<uint32_t*>(o + e) = pack_f16x2(acc[e] * inv, acc[e + 1] * inv);
+    for (int e = 0; e < kPer; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + g * D + e) = pack_f16x2(acc[e] * inv, acc[e + 1] * inv);
+  }
 }
 
 }  // namespace dflash
