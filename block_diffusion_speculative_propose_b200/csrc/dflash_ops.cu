@@ -29,16 +29,17 @@ void launch_append(dflash_handle* h, const AppendParams& p, cudaStream_t st) {
   LaunchScope scope(h, DFLASH_KERNEL_APPEND_KV, st);
   const int heads = 2 * p.Hkv + (p.q ? p.Hq : 0);
   constexpr int kGroups = 512 / D;
-  const int64_t warps4 = static_cast<int64_t>(p.n) * cdiv(heads, 4 * kGroups);
+  const int64_t warps2 = static_cast<int64_t>(p.n) * cdiv(heads, 2 * kGroups);
   // Few rows: one head a lane group, so that the latency of one load and one
-  // store is all a call waits for; else four.
-  if (warps4 < h->num_sms * 8) {
+  // store is all a call waits for; else two (32768 rows of 16 heads: one 89 us,
+  // two 61, four 69).
+  if (warps2 < h->num_sms * 16) {
     const int64_t warps = static_cast<int64_t>(p.n) * cdiv(heads, kGroups);
     launch_k(h->pdl, append_kv_kernel<D, 1>, dim3(static_cast<unsigned>((warps + 3) / 4)),
              dim3(128), 0, st, p);
   } else {
-    const int64_t blocks = std::min<int64_t>((warps4 + 7) / 8, h->num_sms * 32);
-    launch_k(h->pdl, append_kv_kernel<D, 4>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+    const int64_t blocks = std::min<int64_t>((warps2 + 7) / 8, h->num_sms * 32);
+    launch_k(h->pdl, append_kv_kernel<D, 2>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
              st, p);
   }
 }
@@ -138,15 +139,17 @@ dflash_status run_prefix(dflash_handle* h, const PrefixPlan& pl, PartParams p, c
     s = launch_part<D, 2, 128>(h, tq, tk, tv, p, pl.ctas, st);
     own.prefix_ctas = 0;
   }
-  // the own keys' CTAs stay and take one item after another, so that the loads of
-  // the next overlap the end of the last
-  const int64_t ctas = own.prefix_ctas + std::min<int64_t>(
-      static_cast<int64_t>(pl.splits) * p.B * p.Hkv, 2 * h->num_sms);
+  // one CTA an item of own keys: CTAs that stayed and took several items in turn
+  // balanced worse (16 single tokens over 2048 shared keys 36 us against 25)
+  const int64_t ctas = own.prefix_ctas + static_cast<int64_t>(pl.splits) * p.B * p.Hkv;
   if (s == DFLASH_OK && ctas > 0) s = launch_part<D, 1, 64>(h, tq, tk, tv, own, ctas, st);
   if (s != DFLASH_OK) return s;
   LaunchScope scope(h, DFLASH_KERNEL_PREFIX_COMBINE, st);
-  launch_k(h->pdl, attn_join_kernel<D>, dim3(static_cast<unsigned>(
-               (static_cast<int64_t>(p.n_tok) * p.Hkv + 7) / 8)), dim3(256), 0, st, p, pl.nt, o);
+  // a warp a kv group once those fill the card, else a warp a head
+  const int heads = static_cast<int64_t>(p.n_tok) * p.Hkv >= 32 * h->num_sms ? p.G : 1;
+  const int64_t warps = static_cast<int64_t>(p.n_tok) * (p.Hq / heads);
+  launch_k(h->pdl, attn_join_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0,
+           st, p, pl.nt, heads, o);
   return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 

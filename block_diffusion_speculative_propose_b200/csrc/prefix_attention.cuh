@@ -54,7 +54,7 @@ struct PartParams {
   int max_segs;
   float* prefix_o;     // [prefix_ctas][max_segs][NT][128][D]
   float2* prefix_ml;   // [prefix_ctas][max_segs][NT][128]
-  // own keys: (split, request, kv head) items, dealt to the other CTAs in turn
+  // own keys: one CTA a (split, request, kv head)
   int chunk_keys, max_splits, R;          // R = q_len * G
   float* own_o;        // [max_splits][B][Hkv][R][D]
   float2* own_ml;      // [max_splits][B][Hkv][R]
@@ -247,28 +247,22 @@ struct PartWalk {
       ++next;
       return true;
     }
-    // own keys: items (split, request, kv head), the kv head fastest, a grid apart
-    const int stride = static_cast<int>(gridDim.x) - p.prefix_ctas;
-    const int total = p.max_splits * p.B * p.Hkv;
-    for (int i = static_cast<int>(blockIdx.x) - p.prefix_ctas + next * stride; i < total;
-         i += stride) {
-      ++next;
-      const int rest = i / p.Hkv, split = rest / p.B;
-      s.b = rest - split * p.B;
-      const int seq = p.seq_lens[s.b];
-      s.key0 = p.prefix_keys + split * p.chunk_keys;
-      // 64-bit: seq may be anything
-      s.key1 = seq < 0 ? 0
-                       : static_cast<int>(min(static_cast<long long>(seq) + p.q_len,
-                                              static_cast<long long>(s.key0) + p.chunk_keys));
-      if (s.key0 >= s.key1) continue;
-      s.h = i - rest * p.Hkv;
-      s.n_tiles = (s.key1 - s.key0 + KT - 1) / KT;
-      s.tok0 = s.b * p.q_len;
-      s.slot = i;
-      return true;
-    }
-    return false;
+    if (next++ > 0) return false;
+    // own keys: one item (split, request, kv head), the kv head fastest
+    const int i = static_cast<int>(blockIdx.x) - p.prefix_ctas;
+    const int rest = i / p.Hkv, split = rest / p.B;
+    s.b = rest - split * p.B;
+    const int seq = p.seq_lens[s.b];
+    s.key0 = p.prefix_keys + split * p.chunk_keys;
+    // 64-bit: seq may be anything
+    s.key1 = seq < 0 ? 0
+                     : static_cast<int>(min(static_cast<long long>(seq) + p.q_len,
+                                            static_cast<long long>(s.key0) + p.chunk_keys));
+    s.h = i - rest * p.Hkv;
+    s.n_tiles = (s.key1 - s.key0 + KT - 1) / KT;
+    s.tok0 = s.b * p.q_len;
+    s.slot = i;
+    return s.key0 < s.key1;
   }
 };
 
@@ -280,13 +274,35 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   constexpr int NS = C::NS, kHalves = C::kHalves;
   pdl_trigger();
   pdl_wait();
-  PartSeg seg;
-  {
-    PartWalk<NT, KT> first;
-    if (!first.step(p, seg)) return;   // the same for the whole CTA
-  }
-  PartWalk<NT, KT> walk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  PartSeg seg;
+  PartWalk<NT, KT> walk;
+  if (!walk.step(p, seg)) return;   // the same for the whole CTA
+  constexpr int kPages = KT / 16;
+  const int pj = lane % kPages, half = lane / kPages;   // a producer lane's page and column half
+  // row of the pools' [pages * Hkv * 16, D] view where this lane's page of tile t
+  // starts; -16 (zeros are filled in) past the range, the table or the pool
+  auto page_row = [&](int t) {
+    const int key = seg.key0 + t * KT + pj * 16;
+    if (t >= seg.n_tiles || key >= seg.key1) return -16;
+    const int pg = key >> 4;
+    if (pg >= p.W) {
+      raise_error(p.err, DFLASH_DEVERR_TABLE);
+      return -16;
+    }
+    const int page = p.block_table[static_cast<size_t>(max(seg.b, 0)) * p.W + pg];
+    if (page < 0 || page >= p.num_pages) {
+      raise_error(p.err, DFLASH_DEVERR_SLOT);
+      return -16;
+    }
+    return (page * p.Hkv + seg.h) * 16;
+  };
+  // the first pages' numbers come while the CTA sets itself up
+  int row = -16, next_row = -16;
+  if (warp == 0) {
+    row = page_row(0);
+    next_row = page_row(1);
+  }
   extern __shared__ uint8_t part_smem[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(part_smem) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -337,12 +353,14 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    constexpr int kPages = KT / 16;
-    const int pj = lane % kPages, half = lane / kPages;
     const bool loads = lane < kPages * kHalves;
     unsigned seq = 0;      // ring tiles issued
-    bool ok = true;
-    for (int k = 0; ok && walk.step(p, seg); ++k) {
+    bool ok = true, more = true;
+    for (int k = 0; ok && more; ++k) {
+      if (k > 0) {
+        row = page_row(0);
+        next_row = page_row(1);
+      }
       if (lane == 0) {
         ok = mbar_wait(q_empty, (k & 1) ^ 1u, p.err);
         if (ok) {
@@ -354,25 +372,7 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      const int32_t* table = p.block_table + static_cast<size_t>(max(seg.b, 0)) * p.W;
-      // row of the pools' [pages * Hkv * 16, D] view where this lane's page of
-      // tile t starts; -16 (zeros are filled in) past the range, the table or the pool
-      auto page_row = [&](int t) {
-        const int key = seg.key0 + t * KT + pj * 16;
-        if (t >= seg.n_tiles || key >= seg.key1) return -16;
-        const int pg = key >> 4;
-        if (pg >= p.W) {
-          raise_error(p.err, DFLASH_DEVERR_TABLE);
-          return -16;
-        }
-        const int page = table[pg];
-        if (page < 0 || page >= p.num_pages) {
-          raise_error(p.err, DFLASH_DEVERR_SLOT);
-          return -16;
-        }
-        return (page * p.Hkv + seg.h) * 16;
-      };
-      auto issue = [&](const CUtensorMap* map, int row) {
+      auto issue = [&](const CUtensorMap* map, int at) {
         const int s = seq % NS;
         if (lane == 0) {
           ok = mbar_wait(&empty[s], ((seq / NS) & 1) ^ 1u, p.err);
@@ -381,18 +381,18 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         ok = __shfl_sync(0xffffffffu, ok, 0);
         __syncwarp();
         if (ok && loads)
-          tma_load_2d(ring(s) + half * KT * 128 + pj * 2048, map, &full[s], half * 64, row);
+          tma_load_2d(ring(s) + half * KT * 128 + pj * 2048, map, &full[s], half * 64, at);
         ++seq;
       };
-      int row = page_row(0), next = page_row(1);
       if (ok) issue(&tmK, row);
       for (int t = 0; ok && t < seg.n_tiles; ++t) {
         const int after = page_row(t + 2);
-        if (t + 1 < seg.n_tiles) issue(&tmK, next);
+        if (t + 1 < seg.n_tiles) issue(&tmK, next_row);
         if (ok) issue(&tmV, row);
-        row = next;
-        next = after;
+        row = next_row;
+        next_row = after;
       }
+      more = walk.step(p, seg);
     }
     if (!ok && lane == 0) {
       // given up: let the copies in flight land before the CTA's memory goes
@@ -432,7 +432,8 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
         umma_commit(&s_full[buf]);
       };
-      for (int k = 0; ok && walk.step(p, seg); ++k) {
+      bool more_segs = true;
+      for (int k = 0; ok && more_segs; ++k, more_segs = walk.step(p, seg)) {
         const int n_tiles = seg.n_tiles;
         ok = mbar_wait(q_full, k & 1, p.err) && mbar_wait(&full[slot], wraps & 1, p.err);
         if (!ok) break;
@@ -495,7 +496,8 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const float scale = p.scale_log2;
     unsigned tiles = 0, seq = 0;
     bool ok = true;
-    for (int k = 0; walk.step(p, seg); ++k) {
+    bool more = true;
+    for (int k = 0; more; ++k, more = walk.step(p, seg)) {
       // keys that this row sees: none if it is no row of this segment
       int limit = 0;
       {
@@ -635,19 +637,22 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
 }
 
-// One warp joins the parts of a token's kv group (G query heads); prefix_nt: the
-// row tiles of the kernel that ran the prefix.  The lanes read the parts' (m, l)
-// side by side, then every part's row of O with its weight known, so that the
-// loads of a head overlap.
+// One warp joins the parts of `heads` query heads of a token's kv group (all of
+// them, or one where there are few tokens and many parts); prefix_nt: the row
+// tiles of the kernel that ran the prefix.  The lanes read the parts' (m, l) side
+// by side, then every part's row of O with its weight known, so that the loads of
+// a head overlap.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int prefix_nt,
-                                                        f16* __restrict__ out) {
+                                                        int heads, f16* __restrict__ out) {
   pdl_trigger();
   pdl_wait();
   constexpr int kPer = D / 32;
   const int unit = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (unit >= p.n_tok * p.Hkv) return;
-  const int tok = unit / p.Hkv, h = unit - tok * p.Hkv;
+  const int per_tok = p.Hq / heads;
+  if (unit >= p.n_tok * per_tok) return;
+  const int tok = unit / per_tok, head0 = (unit - tok * per_tok) * heads;
+  const int h = head0 / p.G, g0 = head0 - h * p.G;
   const int b = tok / p.q_len, j = tok - b * p.q_len;
   const int seq = p.seq_lens[b];
   if (seq < 0) return;                       // a padding request keeps its rows
@@ -662,7 +667,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int 
     n_prefix = ((item + 1) * p.prefix_tiles - 1) / p.prefix_run - c0 + 1;
   }
   const long long own = static_cast<long long>(seq) + p.q_len - p.prefix_keys;
-  if (own > static_cast<long long>(p.W) * 16 - p.prefix_keys && lane == 0 && j == 0 && h == 0)
+  if (own > static_cast<long long>(p.W) * 16 - p.prefix_keys && lane == 0 && j == 0 && head0 == 0)
     raise_error(p.err, DFLASH_DEVERR_TABLE);
   const int n_own = own <= 0 ? 0
                              : static_cast<int>(min(static_cast<long long>(p.max_splits),
@@ -679,7 +684,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int 
   };
   const size_t first = at(min(lane, max(parts - 1, 0)));
   f16* dst = out + (static_cast<size_t>(tok) * p.Hq + h * p.G) * D + lane * kPer;
-  for (int g = 0; g < p.G; ++g) {
+  for (int g = g0; g < g0 + heads; ++g) {
     float M = -INFINITY, l = 0.f, acc[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
@@ -707,7 +712,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int 
 #pragma unroll
       for (int e = 0; e < kPer; ++e) acc[e] *= keep;
       const int n = min(32, parts - q0);
-#pragma unroll 4
+#pragma unroll 8
       for (int s = 0; s < n; ++s) {
         const float ws = __shfl_sync(0xffffffffu, w, s);
         const float* os = reinterpret_cast<const float*>(

@@ -9,6 +9,7 @@ library is missing this module raises — there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, List, Optional, Sequence
 
@@ -217,19 +218,32 @@ def _rows(t: torch.Tensor, shape, name: str):
     packed inside and any distance apart."""
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
-    if tuple(t.shape[1:]) != tuple(shape):
-        raise ValueError(f"{name}: expected rows of {tuple(shape)}, got {tuple(t.shape[1:])}")
+    size, step = t.shape, t.stride()
+    if size[1:] != shape:
+        raise ValueError(f"{name}: expected rows of {tuple(shape)}, got {tuple(size[1:])}")
     row = 1
-    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size > 1 and step != row:
+    for i in range(len(size) - 1, 0, -1):
+        if size[i] > 1 and step[i] != row:
             raise ValueError(f"{name}: rows must be packed inside")
-        row *= size
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else row)
+        row *= size[i]
+    return t.data_ptr(), (step[0] if size[0] > 1 else row)
+
+
+def _is(t: torch.Tensor, dtype: torch.dtype, shape, name: str) -> int:
+    """The pointer of a packed CUDA tensor of this type and shape."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected {list(shape)}, got {list(t.shape)}")
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor")
+    return t.data_ptr()
 
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle of torch.cuda.current_stream(), without the object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -322,6 +336,10 @@ class DFlash:
                                                ctypes.byref(h)), "dflash_create_vocab_shard")
         self.h = h
         self.ws = Workspace(self.device)
+        # this handle's own query heads, kv heads, head size and page size
+        self._heads = (cfg["n_q_heads"] // self.tp[1], cfg["n_kv_heads"] // self.tp[1],
+                       cfg["head_dim"], cfg.get("page_size", 16))
+        self._prefix_bytes: Dict = {}
 
     def close(self) -> None:
         if getattr(self, "h", None):
@@ -556,35 +574,30 @@ class DFlash:
         the caller projected: optional RMSNorm per head, rotation, and the paged
         scatter (dflash_append_kv).  The rows may be slices of one fused
         projection.  Returns the rotated queries, packed, if q is given."""
-        n, c = int(k.shape[0]), self.cfg
-        hkv, hq, d = c["n_kv_heads"] // self.tp[1], c["n_q_heads"] // self.tp[1], c["head_dim"]
-        for name, t in (("k", k), ("v", v), ("k_norm", k_norm), ("q", q), ("q_norm", q_norm),
-                        ("q_out", q_out), ("k_cache", k_cache), ("v_cache", v_cache)):
-            if t is not None:
-                _want(t, torch.bfloat16, name)
-        _want(positions, torch.int64, "positions")
-        _want(slot_mapping, torch.int64, "slot_mapping")
-        for name, t in (("v", v), ("q", q), ("positions", positions),
-                        ("slot_mapping", slot_mapping)):
-            if t is not None and int(t.shape[0]) != n:
-                raise ValueError(f"{name}: expected {n} rows")
-        for name, t in (("k_norm", k_norm), ("q_norm", q_norm)):
-            if t is not None and t.numel() != d:
-                raise ValueError(f"{name}: expected {d} values")
-        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-            if tuple(t.shape) != (k_cache.shape[0], hkv, c.get("page_size", 16), d):
-                raise ValueError(f"{name}: expected [num_pages, {hkv}, page_size, {d}]")
+        n = k.shape[0]
+        hq, hkv, d, page = self._heads
+        bf = torch.bfloat16
+        for t in (k, v, q):
+            if t is not None and (t.dtype is not bf or t.shape[0] != n):
+                raise ValueError(f"k, v, q: expected {n} rows of bfloat16")
+        pool = (k_cache.shape[0], hkv, page, d)
         kp, ks = _rows(k, (hkv, d), "k")
         vp, vs = _rows(v, (hkv, d), "v")
-        qp, qs = _rows(q, (hq, d), "q") if q is not None else (None, 0)
-        if q is not None and q_out is None:
-            q_out = torch.empty(n, hq, d, dtype=torch.bfloat16, device=self.device)
-        if q_out is not None and tuple(q_out.shape) != (n, hq, d):
-            raise ValueError(f"q_out: expected [{n}, {hq}, {d}]")
-        _check(lib().dflash_append_kv(self.h, kp, ks, vp, vs, _ptr(k_norm), qp, qs, _ptr(q_norm),
-                                      _ptr(q_out), _ptr(positions), _ptr(slot_mapping), n,
-                                      _ptr(k_cache), _ptr(v_cache), int(k_cache.shape[0]),
-                                      _stream(stream)), "dflash_append_kv")
+        qp, qs, op = None, 0, None
+        if q is not None:
+            qp, qs = _rows(q, (hq, d), "q")
+            if q_out is None:
+                q_out = torch.empty(n, hq, d, dtype=bf, device=self.device)
+        if q_out is not None:
+            op = _is(q_out, bf, (n, hq, d), "q_out")
+        _check(lib().dflash_append_kv(
+            self.h, kp, ks, vp, vs,
+            None if k_norm is None else _is(k_norm, bf, (d,), "k_norm"), qp, qs,
+            None if q_norm is None else _is(q_norm, bf, (d,), "q_norm"), op,
+            _is(positions, torch.int64, (n,), "positions"),
+            _is(slot_mapping, torch.int64, (n,), "slot_mapping"), n,
+            _is(k_cache, bf, pool, "k_cache"), _is(v_cache, bf, pool, "v_cache"), pool[0],
+            _stream(stream)), "dflash_append_kv")
         return q_out
 
     def block_attention(self, q, seq_lens, block_table, k_cache, v_cache, o=None,
@@ -613,34 +626,31 @@ class DFlash:
         """Attention of q [B*q_len, Hq, d] over a batch whose first
         ``prefix_pages`` pages (block_table's row 0) are the same for every
         request (dflash_prefix_attention).  Returns o [B*q_len, Hq*d] fp16."""
-        B, W, c = int(seq_lens.shape[0]), int(block_table.shape[1]), self.cfg
-        hkv, hq, d = c["n_kv_heads"] // self.tp[1], c["n_q_heads"] // self.tp[1], c["head_dim"]
-        n = int(q.shape[0])
-        _want(q, torch.bfloat16, "q")
-        _want(seq_lens, torch.int32, "seq_lens")
-        _want(block_table, torch.int32, "block_table")
-        if tuple(q.shape[1:]) != (hq, d) or (n % B if B else n):
+        B, W, n = seq_lens.shape[0], block_table.shape[1], q.shape[0]
+        hq, hkv, d, page = self._heads
+        if n % B if B else n:
             raise ValueError(f"q: expected [{B} * q_len, {hq}, {d}]")
-        if int(block_table.shape[0]) != B:
-            raise ValueError(f"block_table: expected {B} rows")
-        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-            _want(t, torch.bfloat16, name)
-            if tuple(t.shape) != (k_cache.shape[0], hkv, c.get("page_size", 16), d):
-                raise ValueError(f"{name}: expected [num_pages, {hkv}, page_size, {d}]")
+        q_len = n // B if B else 1
         if o is None:
             o = torch.empty(n, hq * d, dtype=torch.float16, device=self.device)
-        _want(o, torch.float16, "o")
-        if o.numel() != n * hq * d:
+        elif o.numel() != n * hq * d:
             raise ValueError(f"o: expected [{n}, {hq * d}]")
-        q_len = n // B if B else 1
         ws = workspace
         if ws is None:
-            ws = self.ws.get(self.prefix_attention_workspace_bytes(B, q_len, W, prefix_pages))
-        _check(lib().dflash_prefix_attention(self.h, _ptr(q), q_len, int(causal), _ptr(seq_lens),
-                                             _ptr(block_table), B, W, prefix_pages, _ptr(k_cache),
-                                             _ptr(v_cache), int(k_cache.shape[0]), _ptr(o),
-                                             _ptr(ws), ws.numel(), _stream(stream)),
-               "dflash_prefix_attention")
+            key = (B, q_len, W, prefix_pages)
+            need = self._prefix_bytes.get(key)
+            if need is None:
+                need = self.prefix_attention_workspace_bytes(*key)
+                self._prefix_bytes[key] = need
+            ws = self.ws.get(need)
+        bf, pool = torch.bfloat16, (k_cache.shape[0], hkv, page, d)
+        _check(lib().dflash_prefix_attention(
+            self.h, _is(q, bf, (n, hq, d), "q"), q_len, int(causal),
+            _is(seq_lens, torch.int32, (B,), "seq_lens"),
+            _is(block_table, torch.int32, (B, W), "block_table"), B, W, prefix_pages,
+            _is(k_cache, bf, pool, "k_cache"), _is(v_cache, bf, pool, "v_cache"), pool[0],
+            _is(o, torch.float16, o.shape, "o"), ws.data_ptr(), ws.numel(), _stream(stream)),
+            "dflash_prefix_attention")
         return o
 
     # ---------------------------------------------------------- diagnostics
@@ -899,15 +909,11 @@ def verify_greedy_noalloc(drafts, target_logits, out_tokens=None, num_accepted=N
 
 def _settings(n: int, temperature, top_k, top_p, min_p):
     """Pointers of the per-row sampling settings, each checked for type and length."""
-    out = []
-    for name, t, dt in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
-                        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
-        if t is not None:
-            _want(t, dt, name)
-            if t.numel() != n:
-                raise ValueError(f"{name}: expected {n} values")
-        out.append(_ptr(t))
-    return out
+    f, shape = torch.float32, (n,)
+    return (None if temperature is None else _is(temperature, f, shape, "temperature"),
+            None if top_k is None else _is(top_k, torch.int32, shape, "top_k"),
+            None if top_p is None else _is(top_p, f, shape, "top_p"),
+            None if min_p is None else _is(min_p, f, shape, "min_p"))
 
 
 def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None,
@@ -917,27 +923,21 @@ def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=Non
     are per-row tensors or None.  Returns the tokens [rows] int32, with
     ``return_probs`` (or ``probs``) the pair (tokens, probabilities)."""
     _want(logits, torch.float32, "logits")
-    _want(u, torch.float32, "u")
     rows, V = logits.shape
     ptr, ld = _rows(logits, (V,), "logits")
-    if u.numel() != rows:
-        raise ValueError(f"u: expected {rows} values")
     if tokens is None:
         tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
     if probs is None and return_probs:
         probs = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    _want(tokens, torch.int32, "tokens")
-    if probs is not None:
-        _want(probs, torch.float32, "probs")
-    if tokens.numel() != rows or (probs is not None and probs.numel() != rows):
-        raise ValueError(f"tokens, probs: expected {rows} values")
-    _check(lib().dflash_sample_tokens(ptr, ld, rows, V,
-                                      *_settings(rows, temperature, top_k, top_p, min_p), _ptr(u),
-                                      _ptr(tokens), _ptr(probs), _ptr(device_error),
-                                      _stream(stream)), "dflash_sample_tokens")
+    _check(lib().dflash_sample_tokens(
+        ptr, ld, rows, V, *_settings(rows, temperature, top_k, top_p, min_p),
+        _is(u, torch.float32, (rows,), "u"), _is(tokens, torch.int32, (rows,), "tokens"),
+        None if probs is None else _is(probs, torch.float32, (rows,), "probs"),
+        _ptr(device_error), _stream(stream)), "dflash_sample_tokens")
     return tokens if probs is None else (tokens, probs)
 
 
+@functools.lru_cache(maxsize=None)
 def verify_sampled_workspace_bytes(B: int, K: int) -> int:
     return lib().dflash_verify_sampled_workspace_bytes(B, K)
 
@@ -949,38 +949,32 @@ def verify_sampled(drafts, target_logits, u_accept, u_sample, temperature=None, 
     (dflash_verify_sampled): ``u_accept`` [B, K] and ``u_sample`` [B] are uniform
     numbers, the settings [B] tensors or None.  Returns (out_tokens, n, bonus),
     as verify_greedy."""
-    _want(drafts, torch.int32, "drafts")
     _want(target_logits, torch.float32, "target_logits")
-    _want(u_accept, torch.float32, "u_accept")
-    _want(u_sample, torch.float32, "u_sample")
     B, K1, V = target_logits.shape
-    K, dev = K1 - 1, target_logits.device
-    if tuple(drafts.shape) != (B, K) or tuple(u_accept.shape) != (B, K) or u_sample.numel() != B:
-        raise ValueError(f"expected drafts and u_accept [{B}, {K}] and u_sample [{B}]")
-    ptr, ld = _rows(target_logits.flatten(0, 1) if B * K1 else target_logits[:, 0], (V,),
-                    "target_logits")
-    if ptr != target_logits.data_ptr():
-        raise ValueError("target_logits: rows must be equally far apart")
+    K, dev, i32 = K1 - 1, target_logits.device, torch.int32
+    step = target_logits.stride()
+    if not target_logits.is_cuda or (V > 1 and step[2] != 1) or (
+            B > 1 and K1 > 1 and step[0] != K1 * step[1]):
+        raise ValueError("target_logits: expected CUDA rows, packed inside, equally far apart")
+    ld = step[1] if K1 > 1 else step[0] if B > 1 else V
     if out_tokens is None:
-        out_tokens = torch.empty(B, K1, dtype=torch.int32, device=dev)
+        out_tokens = torch.empty(B, K1, dtype=i32, device=dev)
     if num_accepted is None:
-        num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        num_accepted = torch.empty(B, dtype=i32, device=dev)
     if bonus is None:
-        bonus = torch.empty(B, dtype=torch.int32, device=dev)
-    for name, t, n in (("out_tokens", out_tokens, B * K1), ("num_accepted", num_accepted, B),
-                       ("bonus", bonus, B)):
-        _want(t, torch.int32, name)
-        if t.numel() != n:
-            raise ValueError(f"{name}: expected {n} values")
+        bonus = torch.empty(B, dtype=i32, device=dev)
     if workspace is None:
         workspace = torch.empty(max(verify_sampled_workspace_bytes(B, K), 256), dtype=torch.uint8,
                                 device=dev)
-    _check(lib().dflash_verify_sampled(_ptr(drafts), ptr, ld, B, K, V,
-                                       *_settings(B, temperature, top_k, top_p, min_p),
-                                       _ptr(u_accept), _ptr(u_sample), _ptr(out_tokens),
-                                       _ptr(num_accepted), _ptr(bonus), _ptr(device_error),
-                                       _ptr(workspace), workspace.numel(), _stream(stream)),
-           "dflash_verify_sampled")
+    _check(lib().dflash_verify_sampled(
+        _is(drafts, i32, (B, K), "drafts"), target_logits.data_ptr(), ld, B, K, V,
+        *_settings(B, temperature, top_k, top_p, min_p),
+        _is(u_accept, torch.float32, (B, K), "u_accept"),
+        _is(u_sample, torch.float32, (B,), "u_sample"),
+        _is(out_tokens, i32, (B, K1), "out_tokens"),
+        _is(num_accepted, i32, (B,), "num_accepted"), _is(bonus, i32, (B,), "bonus"),
+        _ptr(device_error), _ptr(workspace), workspace.numel(), _stream(stream)),
+        "dflash_verify_sampled")
     return out_tokens, num_accepted, bonus
 
 
