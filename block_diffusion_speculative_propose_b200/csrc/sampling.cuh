@@ -76,6 +76,7 @@ struct SmpShared {
   unsigned n_own, own_at;            // this CTA's share of them, its place
   unsigned verdict, more;            // from rank 0
   unsigned found, n_bucket;
+  unsigned run_w[2][kSmpWarps];      // kept border tokens' weights by warp, low and high words
   union {
     unsigned cnt[kSmpBins];          // histogram: tokens
     u64 own[kSmpList];               // this CTA's candidates
@@ -294,11 +295,11 @@ __device__ __forceinline__ void smp_hand_over(int which) {
     st_peer_u64(&sh->list[at + i], 0, sh->own[i]);
 }
 
-__device__ __forceinline__ void smp_clear(bool by_mass) {
+__device__ __forceinline__ void smp_clear(bool tokens, bool weights) {
   SmpShared* sh = smp_shared();
   for (int i = threadIdx.x; i < kSmpBins; i += kSmpThreads) {
-    sh->cnt[i] = 0;
-    if (by_mass) {
+    if (tokens) sh->cnt[i] = 0;
+    if (weights) {
       sh->mass[0][i] = 0;
       sh->mass[1][i] = 0;
     }
@@ -311,15 +312,16 @@ __device__ __forceinline__ void smp_add(unsigned* lo, unsigned* hi, u64 w) {
   const unsigned old = atomicAdd(lo, l);
   atomicAdd(hi, static_cast<unsigned>(w >> 32) + (old + l < old ? 1u : 0u));
 }
-__device__ __forceinline__ void smp_count(unsigned b, bool by_mass, u64 w) {
-  SmpShared* sh = smp_shared();
-  if (by_mass) smp_add(&sh->mass[0][b], &sh->mass[1][b], w);
-  atomicAdd(&sh->cnt[b], 1u);
-}
+
+// Which tokens a histogram's weights stand for, at most: bin b's weigh 2^-(t0 + (b +
+// 0.51) dt) of the largest or more.  dt 0: they are counted.
+struct SmpDepth {
+  double t0, dt;
+};
 
 struct SmpHit {
   unsigned bin;      // in the histogram
-  u64 base, cnt;     // the measure before it, its tokens
+  u64 base, cnt;     // the measure before it, its tokens (counted, or at most)
   u64 all;           // the measure of all bins
   u64 upto;          // tokens before and in it
 };
@@ -330,16 +332,17 @@ struct SmpHit {
 // merges one bin over the CTAs; begins and ends with a cluster barrier, behind
 // which every CTA has the answer.
 __device__ __noinline__ SmpHit smp_find(int rank, bool by_mass, bool falling, u64 base,
-                                        double top_p, double* goal_io) {
+                                        double top_p, SmpDepth depth, double* goal_io) {
   SmpShared* sh = smp_shared();
   const int tid = threadIdx.x;
+  const bool counted = depth.dt == 0.0;
   cluster_sync();
   const int at = rank * kSmpThreads + tid;
   const int b = falling ? kSmpBins - 1 - at : at;
   unsigned n[3][kSmpRanks];
 #pragma unroll
   for (int k = 0; k < kSmpRanks; ++k) {
-    n[0][k] = ld_peer_u32(&sh->cnt[b], k);
+    n[0][k] = counted ? ld_peer_u32(&sh->cnt[b], k) : 0u;
     n[1][k] = by_mass ? ld_peer_u32(&sh->mass[0][b], k) : 0u;
     n[2][k] = by_mass ? ld_peer_u32(&sh->mass[1][b], k) : 0u;
   }
@@ -350,6 +353,9 @@ __device__ __noinline__ SmpHit smp_find(int rank, bool by_mass, bool falling, u6
     v += n[1][k] + (static_cast<u64>(n[2][k]) << 32);
   }
   if (!by_mass) v = c;
+  if (!counted && v)
+    c = static_cast<u64>(static_cast<double>(v) *
+                         exp2(depth.t0 + (b + 0.51) * depth.dt - kSmpOneBits)) + 1;
   const u64 run_v = smp_block_scan(v), run_c = smp_block_scan(c);
   if (tid == kSmpThreads - 1)
     for (int k = 0; k < kSmpRanks; ++k) {
@@ -358,24 +364,23 @@ __device__ __noinline__ SmpHit smp_find(int rank, bool by_mass, bool falling, u6
     }
   cluster_sync();
   SmpHit h;
-  u64 before = base + run_v - v, upto = run_c, all_c = 0;
+  u64 first = run_v - v, upto = run_c;
   h.all = 0;
 #pragma unroll
   for (int k = 0; k < kSmpRanks; ++k) {
     if (k < rank) {
-      before += sh->all_in[0][k];
+      first += sh->all_in[0][k];
       upto += sh->all_in[1][k];
     }
     h.all += sh->all_in[0][k];
-    all_c += sh->all_in[1][k];
   }
   double goal = *goal_io;
   if (top_p >= 0.0) *goal_io = goal = fmax(top_p * static_cast<double>(h.all), 1.0);   // keep one
-  if (c && static_cast<double>(before) < goal &&
-      (static_cast<double>(before + v) >= goal || upto == all_c)) {
+  if (v && static_cast<double>(base + first) < goal &&
+      (static_cast<double>(base + first + v) >= goal || first + v == h.all)) {
     for (int k = 0; k < kSmpRanks; ++k) {
       st_peer_u64(&sh->hit[0], k, b);
-      st_peer_u64(&sh->hit[1], k, before);
+      st_peer_u64(&sh->hit[1], k, base + first);
       st_peer_u64(&sh->hit[2], k, c);
       st_peer_u64(&sh->hit[3], k, upto);
     }
@@ -507,7 +512,7 @@ __device__ __noinline__ u64 smp_border_radix(const SmpRow r, bool by_mass, u64 f
   for (int level = 0; level < 3; ++level) {
     const int bits = level == 2 ? 10 : 11;
     const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
-    smp_clear(by_mass);
+    smp_clear(true, by_mass);
     smp_each(r, [&](const float (&raw)[4], int i) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -518,11 +523,13 @@ __device__ __noinline__ u64 smp_border_radix(const SmpRow r, bool by_mass, u64 f
           continue;
         u64 w = 0;
         if (by_mass && (w = smp_weight(r, x)) == 0) continue;
-        smp_count((o >> shift) & ((1u << bits) - 1), by_mass, w);
+        const uint32_t b = (o >> shift) & ((1u << bits) - 1);
+        if (by_mass) smp_add(&sh->mass[0][b], &sh->mass[1][b], w);
+        atomicAdd(&sh->cnt[b], 1u);
       }
     });
     const SmpHit h = smp_find(r.rank, by_mass, true, base, by_mass && level == 0 ? top_p : -1.0,
-                              &goal);
+                              SmpDepth{0.0, 0.0}, &goal);
     base = h.base;
     ties = h.cnt;
     prefix = (prefix << bits) | h.bin;
@@ -573,48 +580,31 @@ __device__ __noinline__ u64 smp_border_radix(const SmpRow r, bool by_mass, u64 f
   return sh->border[which];
 }
 
-// Tokens of one bin of a histogram into rank 0's list, and of them the border:
-// the first at which `base` and their running measure reach the goal.
-template <class BinAt>
-__device__ __forceinline__ u64 smp_border_in_bin(const SmpRow& r, BinAt bin_at, unsigned bin,
-                                                 bool by_mass, u64 base, double goal, int which) {
-  SmpShared* sh = smp_shared();
-  const int tid = threadIdx.x;
-  if (tid == 0) sh->n_own = 0;
-  __syncthreads();
-  smp_each(r, [&](const float (&x)[4], int i) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (bin_at(x[q], i + q) == bin) smp_candidate(x[q], r.begin + i + q);
-  });
-  smp_hand_over(1 + which);
-  cluster_sync();
-  if (r.rank == 0) {
-    const int n = min(sh->n_list[1 + which], static_cast<unsigned>(kSmpList));
-    for (int i = tid; i < n; i += kSmpThreads)
-      sh->w[i] = by_mass ? smp_weight(r, smp_key_value(sh->list[i])) : 1ull;
-    __syncthreads();
-    u64 before;
-    const int at = smp_cross(n, false, false, base, goal, &before);
-    if (tid < kSmpRanks) st_peer_u64(&sh->border[which], tid, at >= 0 ? sh->list[at] : 0ull);
-  }
-  cluster_sync();
-  return sh->border[which];
-}
-
 // Bins of a search's two levels: of m - x below the maximum, then the parts of
 // the bin in which the border lies.
 struct SmpBinning {
   float m, scale, shift;
   unsigned bin;
   int level;
+  __device__ __forceinline__ unsigned sub(float x) const {
+    const float f = fmaxf(fmaf(m - x, scale, -shift), 0.f);   // 0 .. 1
+    return min(__float_as_uint(fmaf(f, kSmpBins - 2.f, 8388608.f)) - 0x4B000000u, kSmpBins - 1u);
+  }
   // kSmpBins or more: not looked at
   __device__ __forceinline__ unsigned operator()(float x) const {
     const unsigned b = smp_bin(m, scale, x);
     if (level == 0) return b;
-    if (b != bin) return kSmpBins;
-    const float f = fmaxf(fmaf(m - x, scale, -shift), 0.f);   // 0 .. 1
-    return min(__float_as_uint(fmaf(f, kSmpBins - 2.f, 8388608.f)) - 0x4B000000u, kSmpBins - 1u);
+    return b == bin ? sub(x) : kSmpBins;
+  }
+  // before (negative), in (0) or behind bin `at` of the search's last level
+  __device__ __forceinline__ int side(float x, unsigned at) const {
+    const unsigned b = smp_bin(m, scale, x);
+    if (level && b == bin) {
+      const unsigned s = sub(x);
+      return s < at ? -1 : s > at;
+    }
+    const unsigned t = level ? bin : at;
+    return b < t ? -1 : b > t;
   }
   __device__ __forceinline__ void refine(unsigned b) {
     bin = b;
@@ -623,32 +613,77 @@ struct SmpBinning {
   }
 };
 
-// The border of top_k = want: a histogram of linear bins below the maximum, of
-// the bin in which the border lies if that holds more than a list, and the
-// listed tokens themselves.  The radix search where even that holds more (ties).
-__device__ __noinline__ u64 smp_border_k(const SmpRow r, float scale, u64 want) {
+// Where a kept prefix ends: at a key, or (open) still somewhere in a bin, at the
+// token at which `base` and the running measure of the bin's tokens with key >=
+// floor reach the goal.
+struct SmpBorder {
+  u64 key;
+  bool open, by_mass;
+  SmpBinning bins;
+  unsigned bin;
+  u64 base, floor;
+  double goal;
+};
+__device__ __forceinline__ SmpBorder smp_at_key(u64 key) {
+  SmpBorder b;
+  b.key = key;
+  b.open = false;
+  return b;
+}
+
+// The border's key, once the bin's tokens are in rank 0's list n_list[1 + which].
+__device__ __forceinline__ u64 smp_close(const SmpRow& r, const SmpBorder& bd, int which) {
   SmpShared* sh = smp_shared();
-  if (!r.fast) return smp_border_radix(r, false, 0ull, want, 0.0, 0);
-  SmpBinning bins = {r.m, scale, 0.f, 0u, 0};
-  u64 base = 0;
-  double goal = static_cast<double>(want);
+  const int tid = threadIdx.x;
+  smp_hand_over(1 + which);
+  cluster_sync();
+  if (r.rank == 0) {
+    const int n = min(sh->n_list[1 + which], static_cast<unsigned>(kSmpList));
+    for (int i = tid; i < n; i += kSmpThreads)
+      sh->w[i] = bd.by_mass ? smp_weight(r, smp_key_value(sh->list[i])) : 1ull;
+    __syncthreads();
+    u64 before;
+    const int at = smp_cross(n, false, false, bd.base, bd.goal, &before);
+    if (tid < kSmpRanks) st_peer_u64(&sh->border[which], tid, at >= 0 ? sh->list[at] : 0ull);
+  }
+  cluster_sync();
+  return sh->border[which];
+}
+__device__ __forceinline__ u64 smp_resolve(const SmpRow& r, const SmpBorder& bd, int which) {
+  if (!bd.open) return bd.key;
+  if (threadIdx.x == 0) smp_shared()->n_own = 0;
+  __syncthreads();
+  smp_each(r, [&](const float (&x)[4], int i) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (bd.bins.side(x[q], bd.bin) == 0) smp_candidate(x[q], r.begin + i + q);
+  });
+  return smp_close(r, bd, which);
+}
+
+// The border of top_k = want: a histogram of linear bins below the maximum, and of
+// the bin in which the border lies if that holds more than a list.  The radix
+// search where even that holds more (ties).
+__device__ __noinline__ SmpBorder smp_border_k(const SmpRow r, float scale, u64 want) {
+  SmpShared* sh = smp_shared();
+  if (!r.fast) return smp_at_key(smp_border_radix(r, false, 0ull, want, 0.0, 0));
+  SmpBorder bd = {0, true, false, {r.m, scale, 0.f, 0u, 0}, 0, 0, 0, static_cast<double>(want)};
   for (;;) {
-    smp_clear(false);
+    smp_clear(true, false);
     smp_each(r, [&](const float (&x)[4], int) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const unsigned b = bins(x[q]);
+        const unsigned b = bd.bins(x[q]);
         if (b < kSmpBins) atomicAdd(&sh->cnt[b], 1u);
       }
     });
-    const SmpHit h = smp_find(r.rank, false, false, base, -1.0, &goal);
-    if (bins.level == 0 && h.all < want) return 0ull;   // fewer weigh anything: nothing to cut
-    base = h.base;
-    if (h.cnt <= kSmpList)
-      return smp_border_in_bin(r, [&](float x, int) { return bins(x); }, h.bin, false, base, goal,
-                               0);
-    if (bins.level) return smp_border_radix(r, false, 0ull, want, 0.0, 0);
-    bins.refine(h.bin);
+    const SmpHit h = smp_find(r.rank, false, false, bd.base, -1.0, SmpDepth{0.0, 0.0}, &bd.goal);
+    if (bd.bins.level == 0 && h.all < want) return smp_at_key(0ull);   // fewer weigh anything
+    bd.base = h.base;
+    bd.bin = h.bin;
+    if (h.cnt <= kSmpList) return bd;
+    if (bd.bins.level) return smp_at_key(smp_border_radix(r, false, 0ull, want, 0.0, 0));
+    bd.bins.refine(h.bin);
   }
 }
 
@@ -656,24 +691,24 @@ __device__ __noinline__ u64 smp_border_k(const SmpRow r, float scale, u64 want) 
 // of integers are exact, so the bins say exactly where the border lies.  If a
 // list can hold all tokens up to it, the list is filled and the caller draws
 // from it (`listed`; mass_all is the weight of all that top_p refers to).
-__device__ __noinline__ u64 smp_border_p(const SmpRow r, float scale, u64 floor_key,
-                                         double top_p, bool* listed, u64* mass_all) {
+__device__ __noinline__ SmpBorder smp_border_p(const SmpRow r, float scale, u64 floor_key,
+                                               double top_p, bool* listed, u64* mass_all) {
   SmpShared* sh = smp_shared();
   const int tid = threadIdx.x;
   *listed = false;
-  if (!r.fast) return smp_border_radix(r, true, floor_key, 0ull, top_p, 1);
+  if (!r.fast) return smp_at_key(smp_border_radix(r, true, floor_key, 0ull, top_p, 1));
   const float tau = floor_key ? smp_key_value(floor_key) : -INFINITY;
   const int last = floor_key ? static_cast<int>(smp_id(floor_key)) - r.begin : 0x7fffffff;
-  SmpBinning bins = {r.m, scale, 0.f, 0u, 0};
+  SmpBorder bd = {0, true, true, {r.m, scale, 0.f, 0u, 0}, 0, 0, floor_key, 0.0};
   auto bin_at = [&](float x, int i) -> unsigned {
-    const unsigned b = bins(x);
+    const unsigned b = bd.bins(x);
     return floor_key == 0 || x > tau || (x == tau && i <= last) ? b : kSmpBins;
   };
-  u64 base = 0;
-  double goal = 0.0;
+  const double per_bin = r.c / kSmpTab / static_cast<double>(scale);
+  SmpDepth depth = {0.0, per_bin};
   SmpHit h;
   for (;;) {
-    smp_clear(true);
+    smp_clear(false, true);
     smp_each(r, [&](const float (&x)[4], int i) {
       unsigned b[4];
 #pragma unroll
@@ -689,17 +724,19 @@ __device__ __noinline__ u64 smp_border_p(const SmpRow r, float scale, u64 floor_
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (b[q] < kSmpBins) smp_count(b[q], true, w[q]);
+        if (b[q] < kSmpBins) smp_add(&sh->mass[0][b[q]], &sh->mass[1][b[q]], w[q]);
     });
-    h = smp_find(r.rank, true, false, base, bins.level == 0 ? top_p : -1.0, &goal);
-    base = h.base;
-    if (bins.level == 0) {
+    h = smp_find(r.rank, true, false, bd.base, bd.bins.level == 0 ? top_p : -1.0, depth, &bd.goal);
+    bd.base = h.base;
+    bd.bin = h.bin;
+    if (bd.bins.level == 0) {
       *mass_all = h.all;
       if (h.upto <= kSmpList) break;
     }
-    if (h.cnt <= kSmpList) return smp_border_in_bin(r, bin_at, h.bin, true, base, goal, 1);
-    if (bins.level) return smp_border_radix(r, true, floor_key, 0ull, top_p, 1);
-    bins.refine(h.bin);
+    if (h.cnt <= kSmpList) return bd;
+    if (bd.bins.level) return smp_at_key(smp_border_radix(r, true, floor_key, 0ull, top_p, 1));
+    bd.bins.refine(h.bin);
+    depth = {(h.bin - 0.5) * per_bin, per_bin / (kSmpBins - 2)};
   }
   if (tid == 0) sh->n_own = 0;
   __syncthreads();
@@ -714,7 +751,8 @@ __device__ __noinline__ u64 smp_border_p(const SmpRow r, float scale, u64 floor_
   if (r.rank == 0 && tid < kSmpRanks) st_peer_u32(&sh->verdict, tid, sh->n_list[3] <= kSmpList);
   cluster_sync();
   *listed = sh->verdict != 0;
-  return *listed ? floor_key : smp_border_radix(r, true, floor_key, 0ull, top_p, 1);
+  return smp_at_key(*listed ? floor_key
+                            : smp_border_radix(r, true, floor_key, 0ull, top_p, 1));
 }
 
 struct SmpResult {
@@ -736,23 +774,31 @@ __device__ __forceinline__ float smp_share(u64 w, u64 total) {
   return static_cast<float>(static_cast<double>(w) / static_cast<double>(total));
 }
 
-// Draw from the tokens with key >= floor_key in vocabulary order, over all of
-// the row.  draft >= 0: first offered for acceptance with u_accept.
-__device__ __forceinline__ SmpResult smp_draw_row(const SmpRow& r, u64 floor_key, int draft,
+// Draw from the tokens up to the border (all of them unless BORDER) in vocabulary
+// order, over all of the row.  draft >= 0: first offered for acceptance with
+// u_accept.
+template <bool BORDER>
+__device__ __forceinline__ SmpResult smp_draw_row(const SmpRow& r, const SmpBorder& bd, int draft,
                                                   float u_accept, float u) {
   SmpShared* sh = smp_shared();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const float tau = floor_key ? smp_key_value(floor_key) : -INFINITY;
-  const int last = floor_key ? static_cast<int>(smp_id(floor_key)) - r.begin : 0x7fffffff;
-  // kept: above the border's value, or at it and not behind its id
-  auto keep = [&](float x, int i) { return x > tau || (x == tau && i <= last); };
-  auto weight = [&](float x, int i) -> u64 { return keep(x, i) ? smp_weight(r, x) : 0ull; };
   // warps own runs of 128-token groups, a lane four neighbours of a group
   const int seg = ((r.padded >> 7) + kSmpWarps - 1) / kSmpWarps * 128;
   const int beg = min(r.padded, warp * seg), end = min(r.padded, beg + seg);
   const int draft_at = draft - r.begin;
+  const bool open = BORDER && bd.open;
+  u64 floor_key = !BORDER ? 0ull : open ? bd.floor : bd.key;
+  float tau = floor_key ? smp_key_value(floor_key) : -INFINITY;
+  int last = floor_key ? static_cast<int>(smp_id(floor_key)) - r.begin : 0x7fffffff;
+  // kept: above the border's value, or at it and not behind its id
+  auto keep = [&](float x, int i) { return !BORDER || x > tau || (x == tau && i <= last); };
+  auto weight = [&](float x, int i) -> u64 { return keep(x, i) ? smp_weight(r, x) : 0ull; };
+  if (open) {
+    if (tid == 0) sh->n_own = 0;
+    __syncthreads();
+  }
   u64 mine = 0;
-  if (r.fast && r.w_min == 0) {
+  if (r.fast) {
     for (int i0 = beg + lane * 4; i0 < end; i0 += 512) {
       float4 v[4];
 #pragma unroll
@@ -762,17 +808,30 @@ __device__ __forceinline__ SmpResult smp_draw_row(const SmpRow& r, u64 floor_key
       for (int q = 0; q < 4; ++q) {
         const int i = i0 + q * 128;
         if (i >= end) break;
-        const u64 a = smp_bits(r, v[q].x), b = smp_bits(r, v[q].y), c = smp_bits(r, v[q].z),
-                  d = smp_bits(r, v[q].w);
-        if (floor_key == 0) {
-          mine += a + b;
-          mine += c + d;
-          mine -= 4 * kSmpBias;
-        } else {
-          mine += (keep(v[q].x, i) ? a - kSmpBias : 0) + (keep(v[q].y, i + 1) ? b - kSmpBias : 0);
-          mine += (keep(v[q].z, i + 2) ? c - kSmpBias : 0) +
-                  (keep(v[q].w, i + 3) ? d - kSmpBias : 0);
+        const float x[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+        u64 w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = smp_bits(r, x[e]) - kSmpBias;
+        if (r.w_min) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (w[e] < r.w_min) w[e] = 0;
         }
+        if (open) {
+          // what lies before the border's bin is kept; the bin's tokens are listed
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int side = bd.bins.side(x[e], bd.bin);
+            if (side != 0) w[e] = side < 0 ? w[e] : 0;
+            else if (keep(x[e], i + e)) smp_candidate(x[e], r.begin + i + e);
+            if (side == 0) w[e] = 0;
+          }
+        } else if (BORDER) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!keep(x[e], i + e)) w[e] = 0;
+        }
+        mine += (w[0] + w[1]) + (w[2] + w[3]);
       }
     }
   } else {
@@ -780,6 +839,28 @@ __device__ __forceinline__ SmpResult smp_draw_row(const SmpRow& r, u64 floor_key
       const float4 v = smp_load4(r, i);
       mine += weight(v.x, i) + weight(v.y, i + 1) + weight(v.z, i + 2) + weight(v.w, i + 3);
     }
+  }
+  if (open) {
+    // the border among the listed tokens, and the kept ones' weights to their warps
+    floor_key = smp_close(r, bd, bd.by_mass ? 1 : 0);
+    tau = smp_key_value(floor_key);
+    last = static_cast<int>(smp_id(floor_key)) - r.begin;
+    unsigned* lo = sh->run_w[0];
+    unsigned* hi = sh->run_w[1];
+    if (tid < kSmpWarps) lo[tid] = hi[tid] = 0;
+    __syncthreads();
+    // (rank 0 searched in the place of its own list, but has everybody's)
+    const u64* listed = r.rank == 0 ? sh->list : sh->own;
+    const int n = min(r.rank == 0 ? sh->n_list[bd.by_mass ? 2 : 1] : sh->n_own,
+                      static_cast<unsigned>(kSmpList));
+    for (int c = tid; c < n; c += kSmpThreads) {
+      const u64 key = listed[c];
+      const int i = static_cast<int>(smp_id(key)) - r.begin;
+      if (key < floor_key || i >= r.len) continue;
+      smp_add(&lo[i / seg], &hi[i / seg], smp_weight(r, smp_key_value(key)));
+    }
+    __syncthreads();
+    if (lane == 0) mine += lo[warp] + (static_cast<u64>(hi[warp]) << 32);
   }
   const u64 in_warp = warp_sum_u64(mine);
   const u64 upto = smp_block_scan(lane == 0 ? in_warp : 0ull);
@@ -868,6 +949,11 @@ __device__ __forceinline__ SmpResult smp_draw_row(const SmpRow& r, u64 floor_key
     run = sh->bcast[1];
   }
   return out;
+}
+
+__device__ __noinline__ SmpResult smp_draw_bordered(const SmpRow r, const SmpBorder bd, int draft,
+                                                    float u_accept, float u) {
+  return smp_draw_row<true>(r, bd, draft, u_accept, u);
 }
 
 // The same from n candidates in rank 0's list (keys in any order; every token
@@ -1154,7 +1240,9 @@ __device__ __forceinline__ SmpResult smp_row(const float* row, int V, int slice,
   const double below = (r.md - static_cast<double>(r.x_cut)) * r.c;
   r.fast = r.x_cut > -INFINITY && r.m < INFINITY && below >= 46.0 * kSmpTab &&
            below <= 60.0 * kSmpTab;
-  u64 floor_key = 0, mass_all = 0;
+  if (!by_k && !by_p) return smp_draw_row<false>(r, smp_at_key(0ull), draft, u_accept, u);
+  SmpBorder border = smp_at_key(0ull);
+  u64 mass_all = 0;
   bool listed = false;
   if (by_list && r.fast) {
     cut = fmaxf(cut, r.x_cut);         // tokens further down weigh nothing
@@ -1176,10 +1264,12 @@ __device__ __forceinline__ SmpResult smp_row(const float* row, int V, int slice,
     listed = sh->verdict != 0;
   }
   if (!listed) {
-    if (by_k) floor_key = smp_border_k(r, fine, static_cast<u64>(k_in));
-    if (by_p) floor_key = smp_border_p(r, fine, floor_key, top_p, &listed, &mass_all);
+    if (by_k) border = smp_border_k(r, fine, static_cast<u64>(k_in));
+    if (by_p)
+      border = smp_border_p(r, fine, by_k ? smp_resolve(r, border, 0) : 0ull, top_p, &listed,
+                            &mass_all);
   }
-  if (!listed) return smp_draw_row(r, floor_key, draft, u_accept, u);
+  if (!listed) return smp_draw_bordered(r, border, draft, u_accept, u);
   out.writer = 0;
   if (r.rank != 0) return out;
   const bool by_border = mass_all != 0;      // listed by border_p: top_k is done
