@@ -90,9 +90,9 @@ PrefixPlan plan_prefix(const dflash_handle* h, int B, int q_len, int W, int pref
   }
   const size_t pr = static_cast<size_t>(p.ctas) * p.max_segs * p.nt * 128;
   const size_t ow = static_cast<size_t>(p.splits) * B * Hkv * p.R;
-  p.off_ml = align_up(pr * D * 4);
+  p.off_ml = align_up(pr * D * 2);
   p.off_own = p.off_ml + align_up(pr * 8);
-  p.off_own_ml = p.off_own + align_up(ow * D * 4);
+  p.off_own_ml = p.off_own + align_up(ow * D * 2);
   p.total = p.off_own_ml + align_up(ow * 8) + kAlign;
   return p;
 }
@@ -146,7 +146,7 @@ dflash_status run_prefix(dflash_handle* h, const PrefixPlan& pl, PartParams p, c
   if (s != DFLASH_OK) return s;
   LaunchScope scope(h, DFLASH_KERNEL_PREFIX_COMBINE, st);
   // a warp a kv group once those fill the card, else a warp a head
-  const int heads = static_cast<int64_t>(p.n_tok) * p.Hkv >= 32 * h->num_sms ? p.G : 1;
+  const int heads = static_cast<int64_t>(p.n_tok) * p.Hkv >= 16 * h->num_sms ? p.G : 1;
   const int64_t warps = static_cast<int64_t>(p.n_tok) * (p.Hq / heads);
   launch_k(h->pdl, attn_join_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0,
            st, p, pl.nt, heads, o);
@@ -269,12 +269,12 @@ dflash_status dflash_prefix_attention(dflash_handle* h, const void* q, int q_len
   p.prefix_run = static_cast<unsigned>(pl.run);
   p.row_groups = pl.row_groups;
   p.max_segs = pl.max_segs;
-  p.prefix_o = at<float>(workspace, 0);
+  p.prefix_o = at<f16>(workspace, 0);
   p.prefix_ml = at<float2>(workspace, pl.off_ml);
   p.chunk_keys = pl.chunk;
   p.max_splits = pl.splits;
   p.R = pl.R;
-  p.own_o = at<float>(workspace, pl.off_own);
+  p.own_o = at<f16>(workspace, pl.off_own);
   p.own_ml = at<float2>(workspace, pl.off_own_ml);
   p.scale_log2 =
       static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c.head_dim)));

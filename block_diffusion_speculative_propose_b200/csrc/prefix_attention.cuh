@@ -4,6 +4,8 @@
 // o = softmax(q K^T / sqrt(D)) V over the keys of a row is a sum over parts of
 // them: with a reference m, l = sum 2^(s - m) and O = sum 2^(s - m) v of each
 // part (s in units of log2), the whole is sum 2^(m - M) O / sum 2^(m - M) l.
+// A part is left as (m, l) in fp32 and O / l in fp16, the output's type: half the
+// bytes of O in fp32, and the rounding (2^-11) is far below that of P (2^-8).
 // So the shared prefix is one dense attention of every row of the batch against
 // keys that are read once, each request's own keys are another, and a merge
 // joins them.
@@ -52,11 +54,11 @@ struct PartParams {
   int prefix_ctas, prefix_items, prefix_tiles, row_groups;   // row_groups = items per kv head
   unsigned prefix_run;   // units of a CTA; all units fit 31 bits
   int max_segs;
-  float* prefix_o;     // [prefix_ctas][max_segs][NT][128][D]
+  f16* prefix_o;       // [prefix_ctas][max_segs][NT][128][D]
   float2* prefix_ml;   // [prefix_ctas][max_segs][NT][128]
   // own keys: one CTA a (split, request, kv head)
   int chunk_keys, max_splits, R;          // R = q_len * G
-  float* own_o;        // [max_splits][B][Hkv][R][D]
+  f16* own_o;          // [max_splits][B][Hkv][R][D]
   float2* own_ml;      // [max_splits][B][Hkv][R]
   float scale_log2;
   unsigned* err;
@@ -600,10 +602,11 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       if (ok) ok = mbar_wait(&o_full[i], k & 1, p.err);
       tc_fence_after();
       const bool own = seg.b >= 0;
-      float* dst = own ? p.own_o + (static_cast<size_t>(seg.slot) * p.R + r) * D
+      f16* dst = own ? p.own_o + (static_cast<size_t>(seg.slot) * p.R + r) * D
                        : p.prefix_o + ((static_cast<size_t>(seg.slot) * NT + i) * 128 + r) * D;
       const bool store = ok && rows && l != 0.f &&   // a NaN is a result
                          (!own || r < p.R);
+      const float inv = 1.f / l;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         if (!rows) break;
@@ -612,9 +615,14 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         tmem_ld_wait();
         if (store) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(dst + c * 32 + e) =
-                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 32; e += 8) {
+            uint4 w;
+            w.x = pack_f16x2(o[e] * inv, o[e + 1] * inv);
+            w.y = pack_f16x2(o[e + 2] * inv, o[e + 3] * inv);
+            w.z = pack_f16x2(o[e + 4] * inv, o[e + 5] * inv);
+            w.w = pack_f16x2(o[e + 6] * inv, o[e + 7] * inv);
+            *reinterpret_cast<uint4*>(dst + c * 32 + e) = w;
+          }
         }
       }
       tc_fence_before();
@@ -639,15 +647,15 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
 // One warp joins the parts of `heads` query heads of a token's kv group (all of
 // them, or one where there are few tokens and many parts); prefix_nt: the row
-// tiles of the kernel that ran the prefix.  The lanes read the parts' (m, l) side
-// by side, then every part's row of O with its weight known, so that the loads of
-// a head overlap.
+// tiles of the kernel that ran the prefix.  A lane has eight dims of a head (16
+// bytes of a part's row), so a warp has 256 / D heads at once; the loads of four
+// parts are in flight before the first is used.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int prefix_nt,
                                                         int heads, f16* __restrict__ out) {
   pdl_trigger();
   pdl_wait();
-  constexpr int kPer = D / 32;
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
   const int unit = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int per_tok = p.Hq / heads;
   if (unit >= p.n_tok * per_tok) return;
@@ -673,7 +681,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int 
                              : static_cast<int>(min(static_cast<long long>(p.max_splits),
                                                     (own + p.chunk_keys - 1) / p.chunk_keys));
   const int parts = n_prefix + n_own;
-  // lane q: where part q's rows of this group are
+  // where part q's rows of this group are
   auto at = [&](int q) -> size_t {
     if (q < n_prefix) {
       const unsigned c = c0 + q;
@@ -682,56 +690,51 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int 
     }
     return ((static_cast<size_t>(q - n_prefix) * p.B + b) * p.Hkv + h) * p.R + j * p.G;
   };
-  const size_t first = at(min(lane, max(parts - 1, 0)));
-  f16* dst = out + (static_cast<size_t>(tok) * p.Hq + h * p.G) * D + lane * kPer;
-  for (int g = g0; g < g0 + heads; ++g) {
-    float M = -INFINITY, l = 0.f, acc[kPer];
+  const int c8 = lane % kLanes * 8;
+  f16* dst = out + (static_cast<size_t>(tok) * p.Hq + h * p.G) * D + c8;
+  for (int gb = g0; gb < g0 + heads; gb += kAtOnce) {
+    const int g = min(gb + lane / kLanes, g0 + heads - 1);
+    float M = -INFINITY, l = 0.f, acc[8];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-    for (int q0 = 0; q0 < parts; q0 += 32) {
-      const int q = q0 + lane;
-      const size_t mine = (q0 == 0 ? first : q < parts ? at(q) : 0) + g;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      const float* o = nullptr;
-      if (q < parts) {
-        ml = (q < n_prefix ? p.prefix_ml : p.own_ml)[mine];
-        o = (q < n_prefix ? p.prefix_o : p.own_o) + mine * D;
+    for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+    for (int q0 = 0; q0 < parts; q0 += 4) {
+      float2 ml[4];
+      uint4 o[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int q = min(q0 + s, parts - 1);
+        const size_t row = at(q) + g;
+        ml[s] = (q < n_prefix ? p.prefix_ml : p.own_ml)[row];
+        // (a part that saw no key left no row: what is read there is not used)
+        o[s] = *reinterpret_cast<const uint4*>((q < n_prefix ? p.prefix_o : p.own_o) + row * D + c8);
       }
-      if (ml.y == 0.f) ml.x = -INFINITY;       // the row saw no key of this part
-      float top = fmaxf(M, ml.x);
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-      const float keep = M == -INFINITY ? 0.f : part_ex2(M - top);
-      // (a part whose l is NaN keeps its weight whatever its reference)
-      const float w = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : part_ex2(ml.x - top);
-      M = top;
-      float lw = ml.y * w;
+      for (int s = 0; s < 4; ++s) {
+        if (q0 + s >= parts || ml[s].y == 0.f) continue;
+        const float top = fmaxf(M, ml[s].x);
+        const float keep = M == -INFINITY ? 0.f : part_ex2(M - top);
+        // (a part whose l is NaN keeps its weight whatever its reference)
+        const float w = ml[s].y * (ml[s].x == -INFINITY ? 1.f : part_ex2(ml[s].x - top));
+        M = top;
+        l = l * keep + w;
+        const __half2* v = reinterpret_cast<const __half2*>(&o[s]);
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, s);
-      l = l * keep + lw;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] *= keep;
-      const int n = min(32, parts - q0);
-#pragma unroll 8
-      for (int s = 0; s < n; ++s) {
-        const float ws = __shfl_sync(0xffffffffu, w, s);
-        const float* os = reinterpret_cast<const float*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), s));
-        if (ws != 0.f) {
-          float v[kPer];
-          if constexpr (kPer == 4)
-            *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(os + lane * 4);
-          else
-            *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(os + lane * 2);
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) acc[e] += v[e] * ws;
+        for (int c = 0; c < 4; ++c) {
+          const float2 f = __half22float2(v[c]);
+          acc[2 * c] = acc[2 * c] * keep + f.x * w;
+          acc[2 * c + 1] = acc[2 * c + 1] * keep + f.y * w;
         }
       }
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < kPer; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + g * D + e) = pack_f16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (gb + lane / kLanes < g0 + heads) {
+      uint4 w;
+      w.x = pack_f16x2(acc[0] * inv, acc[1] * inv);
+      w.y = pack_f16x2(acc[2] * inv, acc[3] * inv);
+      w.z = pack_f16x2(acc[4] * inv, acc[5] * inv);
+      w.w = pack_f16x2(acc[6] * inv, acc[7] * inv);
+      *reinterpret_cast<uint4*>(dst + static_cast<size_t>(g) * D) = w;
+    }
   }
 }
 
