@@ -642,7 +642,10 @@ class DFlash:
             if need is None:
                 need = self.prefix_attention_workspace_bytes(*key)
                 self._prefix_bytes[key] = need
-            ws = self.ws.get(need)
+            # a captured call keeps scratch of its graph's own: the handle's may
+            # be replaced by a larger one while the graph lives
+            ws = (torch.empty(need, dtype=torch.uint8, device=self.device)
+                  if torch.cuda.is_current_stream_capturing() else self.ws.get(need))
         bf, pool = torch.bfloat16, (k_cache.shape[0], hkv, page, d)
         _check(lib().dflash_prefix_attention(
             self.h, _is(q, bf, (n, hq, d), "q"), q_len, int(causal),
@@ -966,6 +969,8 @@ def verify_sampled(drafts, target_logits, u_accept, u_sample, temperature=None, 
     if workspace is None:
         workspace = torch.empty(max(verify_sampled_workspace_bytes(B, K), 256), dtype=torch.uint8,
                                 device=dev)
+        if isinstance(stream, torch.cuda.Stream):
+            workspace.record_stream(stream)   # scratch is reused only behind that stream's work
     _check(lib().dflash_verify_sampled(
         _is(drafts, i32, (B, K), "drafts"), target_logits.data_ptr(), ld, B, K, V,
         *_settings(B, temperature, top_k, top_p, min_p),

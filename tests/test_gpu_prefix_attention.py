@@ -250,6 +250,48 @@ def test_streams_graph_and_shared_workspace():
     assert torch.equal(o, wa) and h.check_device_errors() == 0
 
 
+def test_captured_call_outlives_a_larger_eager_one():
+    h = handle(32, 8, 128, 3)               # a handle with no scratch yet
+    a = _with(case(32, 8, 128, 1, [40, 50], 2, seed=21), 2)
+    o = torch.zeros(2, 32 * 128, dtype=torch.float16, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        h.prefix_attention(*a, o=o)
+    big = _with(case(32, 8, 128, 16, [900] * 40, 50, seed=22), 50)
+    want_big = check(h, *big)
+    want = check(h, *a)
+    for _ in range(2):
+        o.zero_()
+        g.replay()
+        got_big = h.prefix_attention(*big)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(got_big, want_big)
+
+
+def test_first_request_may_be_padding():
+    h = handle(32, 8, 128)
+    c = case(32, 8, 128, 2, [60, 64, 75], 3, seed=23)
+    seq = c[1].clone()
+    seq[0] = -1                              # its table row still names the prefix
+    check(h, c[0], seq, c[2], 3, c[3], c[4])
+
+
+def test_tensor_parallel_shard_has_its_own_heads():
+    cfg = dict(hidden=256, n_layers=1, n_q_heads=8, n_kv_heads=4, head_dim=64, intermediate=256,
+               vocab=1024, n_target_layers=1, block_size=2, mask_token_id=1023, page_size=16,
+               rms_eps=1e-6, rope_theta=1e6)
+    h = DFlash(cfg, synth.make_weights(cfg, device=DEV), max_position=512, tp=(1, 2))
+    q, seq, table, kc, vc = case(4, 2, 64, 3, [70, 33, 64], 2, seed=24)
+    check(h, q, seq, table, 2, kc, vc)
+    with pytest.raises(ValueError):
+        h.prefix_attention(torch.zeros(9, 8, 64, dtype=BF, device=DEV), seq, table, 2, kc, vc)
+    k = torch.randn(5, 2, 64, device=DEV).to(BF)
+    slots = torch.arange(5, device=DEV)
+    h.append_kv(k, k, slots, slots, kc, vc)
+    assert torch.equal(vc[0, :, :5], k.transpose(0, 1))
+    h.close()
+
+
 def test_bad_pages_are_reported_and_not_read():
     h = handle(4, 2, 64)
     q, seq, table, kc, vc = case(4, 2, 64, 1, [40, 45], 2, seed=13, fill=0.0)

@@ -291,3 +291,35 @@ def test_refusals():
             bad()
     with pytest.raises(DFlashError):
         verify_sampled(drafts, logits, ua, us, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
+
+
+def test_verify_keeps_its_scratch_while_another_stream_runs(monkeypatch):
+    """The scratch of a call on a given stream is not handed to the next
+    allocation before that stream has passed the call."""
+    B, K, V = 8, 4, 1000
+    logits = torch.randn(B, K + 1, V, device=DEV)
+    drafts = torch.randint(0, V, (B, K), device=DEV, dtype=torch.int32)
+    ua, us = torch.rand(B, K, device=DEV), torch.rand(B, device=DEV)
+    temp = torch.ones(B, device=DEV)
+    want = verify_sampled(drafts, logits, ua, us, temperature=temp)
+    torch.cuda.synchronize()
+    scratch, empty = [], torch.empty
+
+    def watched(*a, **kw):
+        t = empty(*a, **kw)
+        if kw.get("dtype") == torch.uint8:
+            scratch.append((t.data_ptr(), t.numel()))
+        return t
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)           # about 0.1 s
+    monkeypatch.setattr(torch, "empty", watched)
+    got = verify_sampled(drafts, logits, ua, us, temperature=temp, stream=side)
+    monkeypatch.setattr(torch, "empty", empty)
+    assert not side.query() and len(scratch) == 1
+    taken = [torch.empty(scratch[0][1], dtype=torch.uint8, device=DEV) for _ in range(32)]
+    assert scratch[0][0] not in [t.data_ptr() for t in taken]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
