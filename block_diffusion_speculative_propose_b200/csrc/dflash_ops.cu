@@ -258,6 +258,9 @@ dflash_status dflash_prefix_attention(dflash_handle* h, const void* q, int q_len
   p.G = c.n_q_heads / c.n_kv_heads;
   p.tpt = pl.tpt;
   p.causal = causal ? 1 : 0;
+  p.q = static_cast<const bf16*>(q);
+  p.k_cache = static_cast<const bf16*>(k_cache);
+  p.v_cache = static_cast<const bf16*>(v_cache);
   p.seq_lens = seq_lens;
   p.block_table = block_table;
   p.W = max_pages_per_seq;

@@ -5,7 +5,9 @@
 // them: with a reference m, l = sum 2^(s - m) and O = sum 2^(s - m) v of each
 // part (s in units of log2), the whole is sum 2^(m - M) O / sum 2^(m - M) l.
 // A part is left as (m, l) in fp32 and O / l in fp16, the output's type: half the
-// bytes of O in fp32, and the rounding (2^-11) is far below that of P (2^-8).
+// bytes of O in fp32, and the rounding (2^-11) is far below that of P (2^-8).  A
+// row with an average past fp16 (the whole may still be inside it) is left in
+// bf16 instead, which -l marks.
 // So the shared prefix is one dense attention of every row of the batch against
 // keys that are read once, each request's own keys are another, and a merge
 // joins them.
@@ -46,6 +48,7 @@ struct PartParams {
   // token t: token t + r / G, query head h * G + r % G
   int B, q_len, n_tok, Hq, Hkv, G, tpt;   // tpt = 128 / G tokens a tile
   int causal;
+  const bf16 *q, *k_cache, *v_cache;
   const int32_t* seq_lens;
   const int32_t* block_table;
   int W, num_pages, prefix_keys;
@@ -54,7 +57,7 @@ struct PartParams {
   int prefix_ctas, prefix_items, prefix_tiles, row_groups;   // row_groups = items per kv head
   unsigned prefix_run;   // units of a CTA; all units fit 31 bits
   int max_segs;
-  f16* prefix_o;       // [prefix_ctas][max_segs][NT][128][D]
+  f16* prefix_o;       // [prefix_ctas][max_segs][NT][128][D] (bf16 rows where l < 0)
   float2* prefix_ml;   // [prefix_ctas][max_segs][NT][128]
   // own keys: one CTA a (split, request, kv head)
   int chunk_keys, max_splits, R;          // R = q_len * G
@@ -357,6 +360,7 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     // ------------------------------------------------------------ TMA producer
     const bool loads = lane < kPages * kHalves;
     unsigned seq = 0;      // ring tiles issued
+    unsigned q_loads = 0;
     bool ok = true, more = true;
     for (int k = 0; ok && more; ++k) {
       if (k > 0) {
@@ -371,6 +375,7 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             for (int hf = 0; hf < kHalves; ++hf)
               part_load_3d(smem + (i * kHalves + hf) * 128 * 128, &tmQ, q_full, hf * 64,
                            seg.h * p.G, seg.tok0 + i * p.tpt);
+          ++q_loads;
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -398,6 +403,9 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
     if (!ok && lane == 0) {
       // given up: let the copies in flight land before the CTA's memory goes
+      for (int spin = 0;
+           q_loads && spin < 100000 && !mbar_test_wait(q_full, (q_loads - 1) & 1); ++spin) {
+      }
       for (unsigned s = seq > NS ? seq - NS : 0; s < seq; ++s)
         for (int spin = 0; spin < 100000 && !mbar_test_wait(&full[s % NS], (s / NS) & 1); ++spin) {
         }
@@ -607,6 +615,7 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const bool store = ok && rows && l != 0.f &&   // a NaN is a result
                          (!own || r < p.R);
       const float inv = 1.f / l;
+      float big = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         if (!rows) break;
@@ -622,16 +631,36 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             w.z = pack_f16x2(o[e + 4] * inv, o[e + 5] * inv);
             w.w = pack_f16x2(o[e + 6] * inv, o[e + 7] * inv);
             *reinterpret_cast<uint4*>(dst + c * 32 + e) = w;
+#pragma unroll
+            for (int a = 0; a < 8; a += 2)
+              big = part_max3(big, fabsf(o[e + a]), fabsf(o[e + a + 1]));
           }
         }
       }
+      // past fp16 (or not finite): the row once more, in bf16
+      const bool wide = store && big * inv > 65504.f;
+      if (__any_sync(0xffffffffu, wide)) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tmem_ld_32x32b_x32(col_o(i) + lanes + c * 32, o);
+          tmem_ld_wait();
+          if (wide) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              *reinterpret_cast<uint32_t*>(dst + c * 32 + e) =
+                  pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+          }
+        }
+      }
+      const float2 stats = make_float2(m, wide ? -l : l);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[i]);
       if (own) {
-        if (r < p.R) p.own_ml[static_cast<size_t>(seg.slot) * p.R + r] = make_float2(m, l);
+        if (r < p.R) p.own_ml[static_cast<size_t>(seg.slot) * p.R + r] = stats;
       } else {
-        p.prefix_ml[(static_cast<size_t>(seg.slot) * NT + i) * 128 + r] = make_float2(m, l);
+        p.prefix_ml[(static_cast<size_t>(seg.slot) * NT + i) * 128 + r] = stats;
       }
       tiles += seg.n_tiles;
       seq += 2 * seg.n_tiles;
@@ -645,14 +674,82 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
 }
 
+// A row whose result is not finite though keys are masked for it: P = 0 times a
+// masked V that is not finite leaves NaN in the product.  If there is such a V,
+// the row is summed again over the keys [0, limit) alone; only broken values reach this, so it is plain: one key a step.
+// The lanes of a head (D / 8, eight dims each) work together.
+template <int D>
+__device__ __noinline__ void attn_row_again(const PartParams& p, int tok, int b, int h, int head,
+                                            int limit, int end, int c8, float* out) {
+  auto row_of = [&](int key) -> int64_t {
+    const int pg = key >> 4;
+    if (pg >= p.W) return -1;
+    const bool shared = key < p.prefix_keys;
+    const int page = p.block_table[static_cast<size_t>(shared ? 0 : b) * p.W + pg];
+    if (page < 0 || page >= p.num_pages) return -1;
+    return ((static_cast<int64_t>(page) * p.Hkv + h) * 16 + (key & 15)) * D + c8;
+  };
+  auto load8 = [](const bf16* src, float* x) {
+    const uint4 w = *reinterpret_cast<const uint4*>(src);
+    const __nv_bfloat162* t = reinterpret_cast<const __nv_bfloat162*>(&w);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float2 f = __bfloat1622float2(t[c]);
+      x[2 * c] = f.x;
+      x[2 * c + 1] = f.y;
+    }
+  };
+  float x[8], qv[8], acc[8];
+  bool bad = false;
+  for (int key = limit; key < end; ++key) {
+    const int64_t at = row_of(key);
+    if (at < 0) continue;
+    load8(p.v_cache + at, x);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) bad |= !(fabsf(x[c]) <= 3.4e38f);
+  }
+  if (!__any_sync(0xffffffffu, bad)) return;      // the row's own result
+  load8(p.q + (static_cast<int64_t>(tok) * p.Hq + head) * D + c8, qv);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  for (int key = 0; key < limit; ++key) {
+    const int64_t at = row_of(key);
+    float s = 0.f;
+    if (at >= 0) {
+      load8(p.k_cache + at, x);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) s += qv[c] * x[c];
+    }
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    s *= p.scale_log2;
+    const float top = fmaxf(m, s), ref = top == -INFINITY ? 0.f : top;
+    const float keep = m == -INFINITY ? 0.f : part_ex2(m - ref), w = part_ex2(s - ref);
+    m = top;
+    l = l * keep + w;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] *= keep;
+    if (at >= 0) {
+      load8(p.v_cache + at, x);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] += w * x[c];
+    }
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) out[c] = acc[c] * inv;
+}
+
 // One warp joins the parts of `heads` query heads of a token's kv group (all of
 // them, or one where there are few tokens and many parts); prefix_nt: the row
 // tiles of the kernel that ran the prefix.  A lane has eight dims of a head (16
 // bytes of a part's row), so a warp has 256 / D heads at once; the loads of four
 // parts are in flight before the first is used.
 template <int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int prefix_nt,
-                                                        int heads, f16* __restrict__ out) {
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ PartParams p,
+                                                        int prefix_nt, int heads,
+                                                        f16* __restrict__ out) {
   pdl_trigger();
   pdl_wait();
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
@@ -677,9 +774,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int 
   const long long own = static_cast<long long>(seq) + p.q_len - p.prefix_keys;
   if (own > static_cast<long long>(p.W) * 16 - p.prefix_keys && lane == 0 && j == 0 && head0 == 0)
     raise_error(p.err, DFLASH_DEVERR_TABLE);
-  const int n_own = own <= 0 ? 0
-                             : static_cast<int>(min(static_cast<long long>(p.max_splits),
-                                                    (own + p.chunk_keys - 1) / p.chunk_keys));
+  const int n_own = own <= 0 || p.max_splits == 0
+                        ? 0
+                        : static_cast<int>(min(static_cast<long long>(p.max_splits),
+                                               (own + p.chunk_keys - 1) / p.chunk_keys));
   const int parts = n_prefix + n_own;
   // where part q's rows of this group are
   auto at = [&](int q) -> size_t {
@@ -690,6 +788,12 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int 
     }
     return ((static_cast<size_t>(q - n_prefix) * p.B + b) * p.Hkv + h) * p.R + j * p.G;
   };
+  // keys that this token sees, and the end of what its parts multiplied
+  const long long all = static_cast<long long>(seq) + p.q_len;
+  const int limit = static_cast<int>(min(all - (p.causal ? p.q_len - j - 1 : 0),
+                                         static_cast<long long>(p.W) * 16));
+  const int end = static_cast<int>(max(min(all, static_cast<long long>(p.W) * 16),
+                                       static_cast<long long>(n_prefix ? p.prefix_keys : 0)));
   const int c8 = lane % kLanes * 8;
   f16* dst = out + (static_cast<size_t>(tok) * p.Hq + h * p.G) * D + c8;
   for (int gb = g0; gb < g0 + heads; gb += kAtOnce) {
@@ -714,25 +818,41 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const PartParams p, int 
         const float top = fmaxf(M, ml[s].x);
         const float keep = M == -INFINITY ? 0.f : part_ex2(M - top);
         // (a part whose l is NaN keeps its weight whatever its reference)
-        const float w = ml[s].y * (ml[s].x == -INFINITY ? 1.f : part_ex2(ml[s].x - top));
+        const float w =
+            fabsf(ml[s].y) * (ml[s].x == -INFINITY ? 1.f : part_ex2(ml[s].x - top));
         M = top;
         l = l * keep + w;
         const __half2* v = reinterpret_cast<const __half2*>(&o[s]);
+        const __nv_bfloat162* wide = reinterpret_cast<const __nv_bfloat162*>(&o[s]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float2 f = __half22float2(v[c]);
+          const float2 f = ml[s].y < 0.f ? __bfloat1622float2(wide[c]) : __half22float2(v[c]);
           acc[2 * c] = acc[2 * c] * keep + f.x * w;
           acc[2 * c + 1] = acc[2 * c + 1] * keep + f.y * w;
         }
       }
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
+    float sum = 0.f;                          // not finite if a value is not
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      acc[c] *= inv;
+      sum += fabsf(acc[c]);
+    }
+    if (limit < end && __any_sync(0xffffffffu, !(sum <= 3.4e38f))) {
+      float again[8];                         // (acc itself stays in registers)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) again[c] = acc[c];
+      attn_row_again<D>(p, tok, b, h, h * p.G + g, limit, end, c8, again);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] = again[c];
+    }
     if (gb + lane / kLanes < g0 + heads) {
       uint4 w;
-      w.x = pack_f16x2(acc[0] * inv, acc[1] * inv);
-      w.y = pack_f16x2(acc[2] * inv, acc[3] * inv);
-      w.z = pack_f16x2(acc[4] * inv, acc[5] * inv);
-      w.w = pack_f16x2(acc[6] * inv, acc[7] * inv);
+      w.x = pack_f16x2(acc[0], acc[1]);
+      w.y = pack_f16x2(acc[2], acc[3]);
+      w.z = pack_f16x2(acc[4], acc[5]);
+      w.w = pack_f16x2(acc[6], acc[7]);
       *reinterpret_cast<uint4*>(dst + static_cast<size_t>(g) * D) = w;
     }
   }

@@ -664,12 +664,14 @@ dflash_status dflash_block_attention(dflash_handle* h, const void* q, const int3
  * to [0, seq_lens[b] + i + 1); seq_lens[b] may end inside the prefix.  A negative
  * seq_lens[b] marks a padding request: its rows of o stay as they were.
  * Scores and sums in fp32; a weight is rounded to bf16 once (2^-8 relative to
- * itself) before it multiplies V.  A value of V that is not finite reaches every
- * row of its request's block, masked or not; other masked or unused places of
- * the pools may hold anything.  Pages outside the pool or past the table
- * (DFLASH_DEVERR_SLOT, DFLASH_DEVERR_TABLE) are not read.
+ * itself) before it multiplies V.  Masked and unused places of the pools may hold
+ * anything, NaN too (a row that a masked V which is not finite met is summed
+ * again, slowly, over the keys it sees).  Pages outside the pool or past the
+ * table (DFLASH_DEVERR_SLOT, DFLASH_DEVERR_TABLE) are not read.
  * q_len * (n_q_heads / n_kv_heads) > 128, B > 65535, max_pages_per_seq > 2^24 or
- * num_pages * n_kv_heads * page_size > 2^31 - 1 is DFLASH_ERR_UNSUPPORTED_SHAPE;
+ * num_pages * n_kv_heads * page_size > 2^31 - 1 is DFLASH_ERR_UNSUPPORTED_SHAPE,
+ * and so is a call of 2^31 pieces (prefix tiles of 64 or 128 keys times kv heads
+ * and 128-row tiles; splits of own keys times requests and kv heads);
  * q, o and the pools are 16-byte aligned, the workspace 256-byte aligned.
  * B == 0 is a no-op.  Needs dflash_prefix_attention_workspace_bytes. */
 size_t dflash_prefix_attention_workspace_bytes(const dflash_handle* h, int B, int q_len,

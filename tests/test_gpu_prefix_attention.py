@@ -211,6 +211,39 @@ def test_minus_infinity_and_nan_in_keys():
     assert o[0].isfinite().all() and o[1, 0].isfinite().all() and o[1, 1, :2].isnan().all()
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (5, 1, 64), (8, 1, 128)])
+def test_values_that_are_not_finite_reach_only_rows_that_see_them(value, hq, hkv, d):
+    h = handle(hq, hkv, d)
+    # the last position of a causal block, in one kv head
+    q, seq, table, kc, vc = case(hq, hkv, d, 4, [40, 45, 61], 2, seed=25)
+    clean = check(h, q, seq, table, 2, kc, vc, causal=True)
+    vc[table[1, 3].long(), 0, 0, 5] = value              # key 48: the last of request 1
+    o = h.prefix_attention(q, seq, table, 2, kc, vc, causal=True)
+    G = hq // hkv
+    hit = torch.zeros(12, hq, d, dtype=torch.bool, device=DEV)
+    hit[7, :G, 5] = True
+    assert not o.view(12, hq, d)[hit].isfinite().any()
+    # rows that do not see it: right within the same bounds; other requests: the same bits
+    rest = ~hit.view(12, -1)
+    vc[table[1, 3].long(), 0, 0, 5] = 0.0
+    want, mag = reference(q, seq, table, 2, kc, vc, True)
+    bound = 2.0 ** -11 * want.abs() + (2.0 ** -8 + 2.0 ** -10) * mag
+    assert ((o.double() - want).abs() <= bound)[rest].all()
+    assert torch.equal(o[:4], clean[:4]) and torch.equal(o[8:], clean[8:])
+    # requests that end inside the prefix, whose last pages hold nothing yet
+    for B, q_len in ((1, 1), (1, 16), (30, 12)):
+        seq_l = [100 - 2 * b for b in range(B)]
+        q, seq, table, kc, vc = case(hq, hkv, d, q_len, seq_l, 12, seed=26)
+        tail = 100 + q_len
+        for j in range(tail // 16, 12):
+            vc[int(table[0, j]), :, tail - 16 * j if tail > 16 * j else 0:] = value
+            kc[int(table[0, j]), :, tail - 16 * j if tail > 16 * j else 0:] = value
+        for causal in (False, True):
+            check(h, q, seq, table, 12, kc, vc, causal=causal)
+    assert h.check_device_errors() == 0
+
+
 @pytest.mark.parametrize("bs", [4, 16])
 def test_agrees_with_block_attention(bs):
     h = handle(32, 8, 128, bs)
@@ -248,6 +281,22 @@ def test_streams_graph_and_shared_workspace():
     o = h.prefix_attention(*a, stream=st)
     st.synchronize()
     assert torch.equal(o, wa) and h.check_device_errors() == 0
+
+
+@pytest.mark.parametrize("B", [2, 40])
+def test_parts_past_the_output_type(B):
+    """V of one part is past fp16 while the whole is inside it: those rows' parts are
+    left in bf16, another 2^-9 of their share of A."""
+    h = handle(32, 8, 128)
+    q, seq, table, kc, vc = case(32, 8, 128, 4, [300 + b for b in range(B)], 18, seed=B)
+    for page in (int(table[0, 17]), int(table[1, 18]), int(table[1, 19])):
+        vc[page, :, :, 40] = 90000.0        # shared keys 272.., own keys of request 1
+    o = h.prefix_attention(q, seq, table, 18, kc, vc)
+    torch.cuda.synchronize()
+    want, mag = reference(q, seq, table, 18, kc, vc, False)
+    assert float(want.abs().max()) < 65504 and float(want.abs().max()) > 2000
+    bound = 2.0 ** -11 * want.abs() + (2.0 ** -8 + 2.0 ** -9 + 2.0 ** -11) * 1.01 * mag
+    assert ((o.double() - want).abs() <= bound).all()
 
 
 def test_captured_call_outlives_a_larger_eager_one():
