@@ -17,15 +17,26 @@
 // Layout.  A cluster takes a row, each of its CTAs a slice.  The first pass
 // brings the row from memory and finds the maxima; whatever the filters then
 // need is read again while it still lies in L2, so a CTA holds no tokens and four
-// of them share an SM, which hides what a row waits for (three cluster barriers
-// and the tail in which one CTA sorts).  What the CTAs have to tell one another
-// is pushed into each other's shared memory before a barrier.
+// of them share an SM, which hides what a row waits for (the cluster barriers and
+// the tail in which one CTA works on a list).  What the CTAs have to tell one
+// another is pushed into each other's shared memory before a barrier.
 //
 // Work.  Only a row without top_k needs the weight of every token (the sums that
 // u and top_p refer to); it costs about nine 64-bit operations.  A top_k needs
 // no second pass: the k-th largest of the threads' own maxima bounds the k-th
 // largest token from below, and only threads whose maximum reaches that bound
-// look at their tokens again.  The candidates, a few more than k, are sorted.
+// look at their tokens again.  The candidates, a few more than k, are ranked in
+// one CTA.
+//
+// Measured (rows of 151936 unless said otherwise), against reading the rows once:
+//   1 row, top_k 20, top_p 0.8       13 us: the chain of barriers and of 64-bit steps
+//   16 rows of a verify              21 us: the same, and the clearing launch
+//   512 rows of 128256, no filter   141 us: 41; the weights' 64-bit operations
+//   320 rows of 128256, top_p 0.9   147 us: 25; two passes over weights, and the
+//                                   histogram's shared-memory additions
+//   128 rows, mixed filters          79 us: 12; the rows with top_p alone
+// A wave is 74 rows (4 CTAs an SM, 8 a row); top_k rows take 20 us of it, rows
+// that need all weights 40 to 75.
 #pragma once
 
 #include "dflash_device.cuh"
@@ -109,6 +120,18 @@ __device__ __forceinline__ u64 smp_key(float x, uint32_t id) {
 }
 __device__ __forceinline__ uint32_t smp_id(u64 key) {
   return 0xffffffffu - static_cast<uint32_t>(key);
+}
+
+// The two halves of a cluster barrier that orders nothing: before a CTA touches a peer's memory the
+// peer must have started: every CTA arrives before it reads the row, and waits when
+// it has something to push, which costs nothing by then.
+__device__ __forceinline__ void smp_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void smp_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
@@ -912,7 +935,7 @@ __device__ __forceinline__ SmpResult smp_draw_row(const SmpRow& r, const SmpBord
   }
   __syncthreads();
   if (sh->found >= kSmpWarps) return out;        // not in this slice
-  // the CTA scans that run together, eight neighbours a thread
+  // the CTA scans that run together, four neighbours a thread
   const int b0 = static_cast<int>(sh->found) * seg, b1 = min(r.padded, b0 + seg);
   run = sh->bcast[0];
   for (int i0 = b0; i0 < b1; i0 += kSmpThreads * 4) {
@@ -1082,7 +1105,7 @@ __device__ __noinline__ SmpResult smp_draw_list(const SmpRow r, int n, int k, do
 }
 
 // One row: maxima, filters, draw.  Exactly one thread of the cluster returns with
-// writer set.
+// writer set.  Entered behind smp_arrive().
 __device__ __forceinline__ SmpResult smp_row(const float* row, int V, int slice,
                                              const SampleSettings& set, int at, int draft,
                                              float u_accept, float u) {
@@ -1180,6 +1203,7 @@ __device__ __forceinline__ SmpResult smp_row(const float* row, int V, int slice,
     }
     __syncthreads();
   }
+  smp_wait();
   if (tid < kSmpRanks) {
     st_peer_u32(&sh->top_in[r.rank], tid, __float_as_uint(top));
 #pragma unroll
@@ -1292,6 +1316,7 @@ struct SampleParams {
 
 // Cluster y draws row y's token.
 __global__ void __launch_bounds__(kSmpThreads, kSmpCtas) sample_kernel(const SampleParams p) {
+  smp_arrive();
   pdl_trigger();
   pdl_wait();
   SmpShared* sh = smp_shared();
@@ -1324,8 +1349,8 @@ struct VerifySampledParams {
 // the row has nothing to say.  Whether it looks only decides if work is saved: a
 // request's answer is its first refusing row's, whoever ran.  The cluster that
 // settles a request's last row writes the answer.  (Runs of two, four or eight
-// rows a cluster, which spare launches, were slower: 128 requests of 16 rows 354,
-// 391 and 413 us against 272, for the rows of one request then wait in line.)
+// rows a cluster, which spare launches, took 1.3 to 1.5 times as long at 128
+// requests of 16 rows, 180 us now: the rows of one request then wait in line.)
 __global__ void __launch_bounds__(kSmpThreads, kSmpCtas)
 verify_sampled_kernel(const VerifySampledParams p) {
   pdl_trigger();
@@ -1338,12 +1363,13 @@ verify_sampled_kernel(const VerifySampledParams p) {
     // one reading for the whole cluster: rank 0's
     if (lead) {
       const unsigned refused = *reinterpret_cast<volatile unsigned*>(p.refused + b);
-      const unsigned told = !(refused && i > K + 1 - static_cast<int>(refused));
-      for (unsigned k = 0; k < kSmpRanks; ++k) st_peer_u32(&sh->more, k, told);
+      sh->more = !(refused && i > K + 1 - static_cast<int>(refused));
     }
     cluster_sync();
-    needed = sh->more != 0;
+    needed = ld_peer_u32(&sh->more, 0) != 0;
   }
+  smp_arrive();
+  if (!needed) smp_wait();   // rank 0 stays until it has been read
   if (needed) {
     const int draft = i < K ? p.drafts[static_cast<int64_t>(b) * K + i] : -1;
     const SmpResult res =

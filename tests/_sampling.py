@@ -20,6 +20,7 @@ def kept(x, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     m = x[order[0]]
     with np.errstate(invalid="ignore"):
         w = np.where(x[order] == m, 1.0, np.exp((x[order] - m) / float(temperature)))
+    w[np.isnan(w)] = 0.0        # infinitely far below, at an infinite temperature
     if min_p > 0:
         ok = w >= float(min_p)
         ok[0] = True

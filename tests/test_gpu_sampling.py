@@ -66,7 +66,8 @@ def check(x, u, **par):
 GRID = [dict(), dict(t=0.0), dict(t=0.7, k=20, p=0.8), dict(k=1), dict(t=1.5, k=50), dict(p=0.9),
         dict(t=1.3, p=0.99), dict(t=0.5, p=0.3), dict(m=0.05), dict(t=2.0, k=1000, p=0.95, m=0.001),
         dict(t=1.0, k=5000), dict(t=1.2, k=3000, p=0.97, m=1e-4), dict(p=0.0), dict(m=1.0),
-        dict(t=20.0, p=0.5), dict(t=1e-3, k=7), dict(t=1e30, p=0.25), dict(t=float("nan"))]
+        dict(t=20.0, p=0.5), dict(t=1e-3, k=7), dict(t=1e30, p=0.25), dict(t=float("nan")),
+        dict(t=float("inf"), p=0.5), dict(t=float("inf"), k=9)]
 
 
 @pytest.mark.parametrize("V", [1, 2, 5, 33, 1000, 1024, 8191, 8193, 32000, 50257, 151936])
