@@ -213,11 +213,11 @@ def _want(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
 
 
-def _rows(t: torch.Tensor, shape, name: str):
-    """(pointer, row stride in elements) of a tensor [n, *shape] whose rows are
-    packed inside and any distance apart."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
+def _rows(t: torch.Tensor, shape, name: str, dev: int):
+    """(pointer, row stride in elements) of a tensor [n, *shape] on CUDA device
+    ``dev`` whose rows are packed inside and any distance apart."""
+    if dev < 0 or t.get_device() != dev:
+        raise ValueError(f"{name}: expected a CUDA tensor on the call's device, got {t.device}")
     size, step = t.shape, t.stride()
     if size[1:] != shape:
         raise ValueError(f"{name}: expected rows of {tuple(shape)}, got {tuple(size[1:])}")
@@ -229,21 +229,24 @@ def _rows(t: torch.Tensor, shape, name: str):
     return t.data_ptr(), (step[0] if size[0] > 1 else row)
 
 
-def _is(t: torch.Tensor, dtype: torch.dtype, shape, name: str) -> int:
-    """The pointer of a packed CUDA tensor of this type and shape."""
+def _is(t: torch.Tensor, dtype: torch.dtype, shape, name: str, dev: int) -> int:
+    """The pointer of a packed tensor of this type and shape on CUDA device ``dev``."""
     if t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected {list(shape)}, got {list(t.shape)}")
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError(f"{name}: expected a contiguous CUDA tensor")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor on the call's CUDA device, "
+                         f"got {t.device}")
     return t.data_ptr()
 
 
-def _stream(stream) -> int:
+def _stream(stream, dev: Optional[int] = None) -> int:
+    """A stream's raw handle; None: the current stream, of device ``dev`` if given."""
     if stream is None:
         # the raw handle of torch.cuda.current_stream(), without the object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()
+                                                  if dev is None else dev)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -336,9 +339,9 @@ class DFlash:
                                                ctypes.byref(h)), "dflash_create_vocab_shard")
         self.h = h
         self.ws = Workspace(self.device)
-        # this handle's own query heads, kv heads, head size and page size
+        # this handle's own query heads, kv heads, head size, page size and device
         self._heads = (cfg["n_q_heads"] // self.tp[1], cfg["n_kv_heads"] // self.tp[1],
-                       cfg["head_dim"], cfg.get("page_size", 16))
+                       cfg["head_dim"], cfg.get("page_size", 16), device)
         self._prefix_bytes: Dict = {}
 
     def close(self) -> None:
@@ -575,29 +578,30 @@ class DFlash:
         scatter (dflash_append_kv).  The rows may be slices of one fused
         projection.  Returns the rotated queries, packed, if q is given."""
         n = k.shape[0]
-        hq, hkv, d, page = self._heads
+        hq, hkv, d, page, dev = self._heads
         bf = torch.bfloat16
         for t in (k, v, q):
             if t is not None and (t.dtype is not bf or t.shape[0] != n):
                 raise ValueError(f"k, v, q: expected {n} rows of bfloat16")
         pool = (k_cache.shape[0], hkv, page, d)
-        kp, ks = _rows(k, (hkv, d), "k")
-        vp, vs = _rows(v, (hkv, d), "v")
+        kp, ks = _rows(k, (hkv, d), "k", dev)
+        vp, vs = _rows(v, (hkv, d), "v", dev)
         qp, qs, op = None, 0, None
         if q is not None:
-            qp, qs = _rows(q, (hq, d), "q")
+            qp, qs = _rows(q, (hq, d), "q", dev)
             if q_out is None:
                 q_out = torch.empty(n, hq, d, dtype=bf, device=self.device)
         if q_out is not None:
-            op = _is(q_out, bf, (n, hq, d), "q_out")
+            op = _is(q_out, bf, (n, hq, d), "q_out", dev)
         _check(lib().dflash_append_kv(
             self.h, kp, ks, vp, vs,
-            None if k_norm is None else _is(k_norm, bf, (d,), "k_norm"), qp, qs,
-            None if q_norm is None else _is(q_norm, bf, (d,), "q_norm"), op,
-            _is(positions, torch.int64, (n,), "positions"),
-            _is(slot_mapping, torch.int64, (n,), "slot_mapping"), n,
-            _is(k_cache, bf, pool, "k_cache"), _is(v_cache, bf, pool, "v_cache"), pool[0],
-            _stream(stream)), "dflash_append_kv")
+            None if k_norm is None else _is(k_norm, bf, (d,), "k_norm", dev), qp, qs,
+            None if q_norm is None else _is(q_norm, bf, (d,), "q_norm", dev), op,
+            _is(positions, torch.int64, (n,), "positions", dev),
+            _is(slot_mapping, torch.int64, (n,), "slot_mapping", dev), n,
+            _is(k_cache, bf, pool, "k_cache", dev),
+            _is(v_cache, bf, pool, "v_cache", dev), pool[0],
+            _stream(stream, dev)), "dflash_append_kv")
         return q_out
 
     def block_attention(self, q, seq_lens, block_table, k_cache, v_cache, o=None,
@@ -627,7 +631,7 @@ class DFlash:
         ``prefix_pages`` pages (block_table's row 0) are the same for every
         request (dflash_prefix_attention).  Returns o [B*q_len, Hq*d] fp16."""
         B, W, n = seq_lens.shape[0], block_table.shape[1], q.shape[0]
-        hq, hkv, d, page = self._heads
+        hq, hkv, d, page, dev = self._heads
         if n % B if B else n:
             raise ValueError(f"q: expected [{B} * q_len, {hq}, {d}]")
         q_len = n // B if B else 1
@@ -648,11 +652,13 @@ class DFlash:
                   if torch.cuda.is_current_stream_capturing() else self.ws.get(need))
         bf, pool = torch.bfloat16, (k_cache.shape[0], hkv, page, d)
         _check(lib().dflash_prefix_attention(
-            self.h, _is(q, bf, (n, hq, d), "q"), q_len, int(causal),
-            _is(seq_lens, torch.int32, (B,), "seq_lens"),
-            _is(block_table, torch.int32, (B, W), "block_table"), B, W, prefix_pages,
-            _is(k_cache, bf, pool, "k_cache"), _is(v_cache, bf, pool, "v_cache"), pool[0],
-            _is(o, torch.float16, o.shape, "o"), ws.data_ptr(), ws.numel(), _stream(stream)),
+            self.h, _is(q, bf, (n, hq, d), "q", dev), q_len, int(causal),
+            _is(seq_lens, torch.int32, (B,), "seq_lens", dev),
+            _is(block_table, torch.int32, (B, W), "block_table", dev), B, W, prefix_pages,
+            _is(k_cache, bf, pool, "k_cache", dev),
+            _is(v_cache, bf, pool, "v_cache", dev), pool[0],
+            _is(o, torch.float16, o.shape, "o", dev), ws.data_ptr(), ws.numel(),
+            _stream(stream, dev)),
             "dflash_prefix_attention")
         return o
 
@@ -910,13 +916,13 @@ def verify_greedy_noalloc(drafts, target_logits, out_tokens=None, num_accepted=N
     return out_tokens, num_accepted, bonus
 
 
-def _settings(n: int, temperature, top_k, top_p, min_p):
+def _settings(n: int, temperature, top_k, top_p, min_p, dev: int):
     """Pointers of the per-row sampling settings, each checked for type and length."""
     f, shape = torch.float32, (n,)
-    return (None if temperature is None else _is(temperature, f, shape, "temperature"),
-            None if top_k is None else _is(top_k, torch.int32, shape, "top_k"),
-            None if top_p is None else _is(top_p, f, shape, "top_p"),
-            None if min_p is None else _is(min_p, f, shape, "min_p"))
+    return (None if temperature is None else _is(temperature, f, shape, "temperature", dev),
+            None if top_k is None else _is(top_k, torch.int32, shape, "top_k", dev),
+            None if top_p is None else _is(top_p, f, shape, "top_p", dev),
+            None if min_p is None else _is(min_p, f, shape, "min_p", dev))
 
 
 def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None,
@@ -926,17 +932,18 @@ def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=Non
     are per-row tensors or None.  Returns the tokens [rows] int32, with
     ``return_probs`` (or ``probs``) the pair (tokens, probabilities)."""
     _want(logits, torch.float32, "logits")
-    rows, V = logits.shape
-    ptr, ld = _rows(logits, (V,), "logits")
+    (rows, V), dev = logits.shape, logits.get_device()
+    ptr, ld = _rows(logits, (V,), "logits", dev)
     if tokens is None:
         tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
     if probs is None and return_probs:
         probs = torch.empty(rows, dtype=torch.float32, device=logits.device)
     _check(lib().dflash_sample_tokens(
-        ptr, ld, rows, V, *_settings(rows, temperature, top_k, top_p, min_p),
-        _is(u, torch.float32, (rows,), "u"), _is(tokens, torch.int32, (rows,), "tokens"),
-        None if probs is None else _is(probs, torch.float32, (rows,), "probs"),
-        _ptr(device_error), _stream(stream)), "dflash_sample_tokens")
+        ptr, ld, rows, V, *_settings(rows, temperature, top_k, top_p, min_p, dev),
+        _is(u, torch.float32, (rows,), "u", dev),
+        _is(tokens, torch.int32, (rows,), "tokens", dev),
+        None if probs is None else _is(probs, torch.float32, (rows,), "probs", dev),
+        _ptr(device_error), _stream(stream, dev)), "dflash_sample_tokens")
     return tokens if probs is None else (tokens, probs)
 
 
@@ -954,31 +961,33 @@ def verify_sampled(drafts, target_logits, u_accept, u_sample, temperature=None, 
     as verify_greedy."""
     _want(target_logits, torch.float32, "target_logits")
     B, K1, V = target_logits.shape
-    K, dev, i32 = K1 - 1, target_logits.device, torch.int32
+    K, dev, i32 = K1 - 1, target_logits.get_device(), torch.int32
     step = target_logits.stride()
     if not target_logits.is_cuda or (V > 1 and step[2] != 1) or (
             B > 1 and K1 > 1 and step[0] != K1 * step[1]):
         raise ValueError("target_logits: expected CUDA rows, packed inside, equally far apart")
     ld = step[1] if K1 > 1 else step[0] if B > 1 else V
+    device = target_logits.device
     if out_tokens is None:
-        out_tokens = torch.empty(B, K1, dtype=i32, device=dev)
+        out_tokens = torch.empty(B, K1, dtype=i32, device=device)
     if num_accepted is None:
-        num_accepted = torch.empty(B, dtype=i32, device=dev)
+        num_accepted = torch.empty(B, dtype=i32, device=device)
     if bonus is None:
-        bonus = torch.empty(B, dtype=i32, device=dev)
+        bonus = torch.empty(B, dtype=i32, device=device)
     if workspace is None:
         workspace = torch.empty(max(verify_sampled_workspace_bytes(B, K), 256), dtype=torch.uint8,
-                                device=dev)
-        if isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)   # scratch is reused only behind that stream's work
+                                device=device)
+        if stream is not None:                # scratch is reused only behind that stream's work
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                    torch.cuda.ExternalStream(int(stream), device=device))
     _check(lib().dflash_verify_sampled(
-        _is(drafts, i32, (B, K), "drafts"), target_logits.data_ptr(), ld, B, K, V,
-        *_settings(B, temperature, top_k, top_p, min_p),
-        _is(u_accept, torch.float32, (B, K), "u_accept"),
-        _is(u_sample, torch.float32, (B,), "u_sample"),
-        _is(out_tokens, i32, (B, K1), "out_tokens"),
-        _is(num_accepted, i32, (B,), "num_accepted"), _is(bonus, i32, (B,), "bonus"),
-        _ptr(device_error), _ptr(workspace), workspace.numel(), _stream(stream)),
+        _is(drafts, i32, (B, K), "drafts", dev), target_logits.data_ptr(), ld, B, K, V,
+        *_settings(B, temperature, top_k, top_p, min_p, dev),
+        _is(u_accept, torch.float32, (B, K), "u_accept", dev),
+        _is(u_sample, torch.float32, (B,), "u_sample", dev),
+        _is(out_tokens, i32, (B, K1), "out_tokens", dev),
+        _is(num_accepted, i32, (B,), "num_accepted", dev), _is(bonus, i32, (B,), "bonus", dev),
+        _ptr(device_error), _ptr(workspace), workspace.numel(), _stream(stream, dev)),
         "dflash_verify_sampled")
     return out_tokens, num_accepted, bonus
 

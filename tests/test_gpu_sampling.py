@@ -294,7 +294,8 @@ def test_refusals():
         verify_sampled(drafts, logits, ua, us, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
 
 
-def test_verify_keeps_its_scratch_while_another_stream_runs(monkeypatch):
+@pytest.mark.parametrize("raw", [False, True])
+def test_verify_keeps_its_scratch_while_another_stream_runs(monkeypatch, raw):
     """The scratch of a call on a given stream is not handed to the next
     allocation before that stream has passed the call."""
     B, K, V = 8, 4, 1000
@@ -316,7 +317,8 @@ def test_verify_keeps_its_scratch_while_another_stream_runs(monkeypatch):
     with torch.cuda.stream(side):
         torch.cuda._sleep(200_000_000)           # about 0.1 s
     monkeypatch.setattr(torch, "empty", watched)
-    got = verify_sampled(drafts, logits, ua, us, temperature=temp, stream=side)
+    got = verify_sampled(drafts, logits, ua, us, temperature=temp,
+                         stream=side.cuda_stream if raw else side)
     monkeypatch.setattr(torch, "empty", empty)
     assert not side.query() and len(scratch) == 1
     taken = [torch.empty(scratch[0][1], dtype=torch.uint8, device=DEV) for _ in range(32)]
@@ -324,3 +326,12 @@ def test_verify_keeps_its_scratch_while_another_stream_runs(monkeypatch):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_tensors_of_another_device_are_refused():
+    x, u = torch.randn(2, 50, device=DEV), torch.rand(2, device=DEV)
+    for bad in (lambda: sample_tokens(x.cpu(), u), lambda: sample_tokens(x, u.cpu()),
+                lambda: sample_tokens(x, u, temperature=full(2, 1.0).cpu()),
+                lambda: sample_tokens(x, u, tokens=torch.zeros(2, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            bad()
