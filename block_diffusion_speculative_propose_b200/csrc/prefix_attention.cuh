@@ -14,6 +14,8 @@
 //   prefix   bound by the tensor cores: 4 D flops a row and key, the keys read
 //            once per 256 rows from L2
 //   own keys bound by HBM: 4 D bytes a key and kv head
+// P is rounded to bf16 once, 2^-8 of each weight: a second product for what that
+// leaves would add half to the tensor time, five sixths of a large call.
 //
 // attn_part_kernel<D, NT, KT> runs both.  NT row tiles of 128 query rows share
 // the K/V tiles of KT keys that pass through a ring in shared memory; S and,

@@ -25,6 +25,11 @@
  *   dflash_spec_step, dflash_step_graph_* — the four calls above as one step with
  *                            nothing from the host between them, eager or as one
  *                            CUDA graph owned by the library.
+ *   dflash_append_kv, dflash_prefix_attention, dflash_sample_tokens,
+ *   dflash_verify_sampled — beside the pages' greedy path: caches and attention
+ *                            for layers that the caller projects itself over a
+ *                            shared prompt, and the same two decoding steps for a
+ *                            target that samples.
  *   dflash_create_vocab_shard, dflash_propose_keys, dflash_finalize_draft_keys —
  *                            §"DFlashQwen3ForCausalLM": the aliased LM head split over
  *                            the vocabulary across tensor-parallel ranks, combined
