@@ -136,6 +136,33 @@ def test_zeros_and_infinities_stay_in_their_heads():
     h.close()
 
 
+def test_offsets_past_32_bits():
+    """Rows 2^30 elements apart, slots past element 2^31 of the pools."""
+    hq, hkv, d, n = 32, 8, 128, 5
+    h = handle(hq, hkv, d)
+    q, k, v, _, _, _, pos, kn, qn = inputs(n, hq, hkv, d, seed=9, fused=False)
+    far = torch.empty((n - 1) * 2 ** 30 + hq * d, dtype=BF, device=DEV)
+    rows = lambda x: far.as_strided((n, *x.shape[1:]), (2 ** 30, d, 1))  # noqa: E731
+    pages = 2 ** 31 // (hkv * 16 * d) + 40
+    kc = torch.empty(pages, hkv, 16, d, dtype=BF, device=DEV)
+    vc = torch.empty_like(kc)
+    slots = torch.tensor([3, pages * 16 - 1, pages * 16 - 200, 2 ** 31 // (hkv * d), 700], device=DEV)
+    page, off = slots // 16, slots % 16
+    for x in (k, v):                              # keys far apart, then values
+        rows(x).copy_(x)
+        h.append_kv(rows(k) if x is k else k, rows(v) if x is v else v, pos, slots, kc, vc,
+                    k_norm=kn)
+        want, bound = formula(k, kn, pos)
+        assert ((kc[page, :, off].double() - want).abs() <= bound).all()
+        assert torch.equal(vc[page, :, off], v)
+    rows(q).copy_(q)
+    got = h.append_kv(k, v, pos, slots, kc, vc, k_norm=kn, q=rows(q), q_norm=qn)
+    want, bound = formula(q, qn, pos)
+    assert ((got.double() - want).abs() <= bound).all()
+    assert h.check_device_errors() == 0
+    h.close()
+
+
 def test_in_place_query_other_stream_and_graph():
     h = handle(8, 2, 128)
     q, k, v, kc, vc, slots, pos, kn, qn = inputs(40, 8, 2, 128, seed=4, fused=False)

@@ -171,6 +171,33 @@ def test_long_own_keys_and_wide_tables():
     check(h, *_with(case(32, 8, 128, 1, [40000], 2400, seed=6), 2400))
 
 
+def test_pages_past_32_bits_of_a_pool():
+    h = handle(32, 8, 128)
+    for q_len, B in ((1, 2), (4, 40)):
+        q, seq, table, kc, vc = case(32, 8, 128, q_len, [200 + b for b in range(B)], 8, seed=27)
+        pages = 2 ** 31 // (8 * 16 * 128) + kc.shape[0]
+        big_k = torch.empty(pages, 8, 16, 128, dtype=BF, device=DEV)
+        big_v = torch.empty_like(big_k)
+        first = pages - kc.shape[0]              # every page past element 2^31
+        big_k[first:], big_v[first:] = kc, vc
+        moved = torch.where(table >= 0, table + first, table)
+        want = h.prefix_attention(q, seq, table, 8, kc, vc, causal=True)
+        got = h.prefix_attention(q, seq, moved, 8, big_k, big_v, causal=True)
+        assert torch.equal(got, want)
+        check(h, q, seq, table, 8, kc, vc, causal=True)
+        # a masked value that is not finite is found there too
+        last = int(seq[1]) + q_len - 1
+        page = int(moved[1, last // 16])
+        big_v[page, :, last % 16] = float("nan")
+        got = h.prefix_attention(q, seq, moved, 8, big_k, big_v, causal=True)
+        exact, mag = reference(q, seq, table, 8, kc, vc, True)
+        bound = 2.0 ** -11 * exact.abs() + (2.0 ** -8 + 2.0 ** -10) * mag
+        near = ((got.double() - exact).abs() <= bound).view(B, q_len, -1)
+        assert near[1, :-1].all()
+        assert torch.equal(got.view(B, q_len, -1)[2:], want.view(B, q_len, -1)[2:])
+    assert h.check_device_errors() == 0
+
+
 def test_padding_requests_keep_their_rows():
     h = handle(32, 8, 128)
     c = case(32, 8, 128, 4, [60, 64, 75, 90, 48, 50], 3, seed=7)

@@ -186,6 +186,22 @@ def test_verify_rules(B, K, V, par):
     check_verify(*verify_inputs(B, K, V, seed=B + K), **settings_of(B, **par))
 
 
+def test_rows_past_32_bits():
+    V, ld = 5000, 2 ** 30
+    far = torch.empty(2 * ld + V, device=DEV)
+    drafts, logits, ua, us = verify_inputs(1, 2, V, 41, likely=1.0)
+    ua.zero_()                                    # the last row decides
+    rows = far.as_strided((3, V), (ld, 1))
+    rows.copy_(logits[0])
+    u = torch.rand(3, generator=rng(42), device=DEV)
+    for par in (dict(), dict(k=20, p=0.9), dict(p=0.8), dict(t=0.0)):
+        check(rows, u, **settings_of(3, **par))
+        want = verify_sampled(drafts, logits, ua, us, **settings_of(1, **par))
+        got = verify_sampled(drafts, rows.view(1, 3, V), ua, us, **settings_of(1, **par))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def test_verify_greedy_rows_decide_as_verify_greedy():
     drafts, logits, ua, us = verify_inputs(9, 15, 5000, 2, likely=0.9)
     logits[2, 3] = logits[2, 3].round()
