@@ -73,17 +73,25 @@ PrefixPlan plan_prefix(const dflash_handle* h, int B, int q_len, int W, int pref
     p.items = Hkv * p.row_groups;
     p.tiles = cdiv(prefix_pages * 16, p.kt);
     const int64_t units = static_cast<int64_t>(p.items) * p.tiles;
-    const int slots = p.nt == 2 ? h->num_sms : 2 * h->num_sms;
+    // One row tile leaves half of the CTAs that fit to the requests' own keys, and a
+    // CTA at least 256 keys: its start costs as much as six tiles (16 single tokens
+    // over 2048 shared keys, runs of two, four and eight tiles: 23.3, 17.7, 17.7 us).
+    const int slots = h->num_sms;
     p.too_many = units > INT32_MAX;
-    p.run = std::max<int64_t>(2, (units + slots - 1) / slots);
+    p.run = std::max<int64_t>(p.nt == 2 ? 2 : 4, (units + slots - 1) / slots);
     p.ctas = static_cast<int>((units + p.run - 1) / p.run);
     p.max_segs = static_cast<int>((p.run - 1) / p.tiles + 2);
   }
   const int own_keys = (W - prefix_pages) * 16;
   if (own_keys > 0) {
-    const double est = static_cast<double>(B) * Hkv * own_keys;
-    int chunk = static_cast<int>(std::ceil(est / (8.0 * h->num_sms)));
-    chunk = std::max(128, std::min(8192, (chunk + 63) / 64 * 64));
+    // Two CTAs an SM if each has 2048 keys or less, for a CTA's start costs as much
+    // as six tiles (32 requests of up to 2048 own keys in chunks of 448 against 1792:
+    // 147 us against 127); else shorter ones, down to an eighth of an SM's share,
+    // which balance requests of different lengths (100 of up to 8000: chunks of 8192
+    // 398 us, of 5568 325).
+    const double per_sm = static_cast<double>(B) * Hkv * own_keys / h->num_sms;
+    int chunk = static_cast<int>(std::ceil(std::max(per_sm / 8, std::min(per_sm / 2, 2048.0))));
+    chunk = std::max(256, std::min(8192, (chunk + 63) / 64 * 64));
     p.chunk = chunk;
     p.splits = cdiv(own_keys, chunk);
     p.too_many |= static_cast<int64_t>(p.splits) * B * Hkv > INT32_MAX / 2;

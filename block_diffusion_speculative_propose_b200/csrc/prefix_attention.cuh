@@ -746,8 +746,8 @@ __device__ __noinline__ void attn_row_again(const PartParams& p, int tok, int b,
 // One warp joins the parts of `heads` query heads of a token's kv group (all of
 // them, or one where there are few tokens and many parts); prefix_nt: the row
 // tiles of the kernel that ran the prefix.  A lane has eight dims of a head (16
-// bytes of a part's row), so a warp has 256 / D heads at once; the loads of four
-// parts are in flight before the first is used.
+// bytes of a part's row), so a warp has 256 / D heads at once, or as many shares of
+// one head's parts; the loads of four parts are in flight before the first is used.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ PartParams p,
                                                         int prefix_nt, int heads,
@@ -798,17 +798,19 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
                                        static_cast<long long>(n_prefix ? p.prefix_keys : 0)));
   const int c8 = lane % kLanes * 8;
   f16* dst = out + (static_cast<size_t>(tok) * p.Hq + h * p.G) * D + c8;
+  // one head: the lane groups take its parts in turn
+  const int share = heads == 1 ? kAtOnce : 1, mine = heads == 1 ? lane / kLanes : 0;
   for (int gb = g0; gb < g0 + heads; gb += kAtOnce) {
     const int g = min(gb + lane / kLanes, g0 + heads - 1);
     float M = -INFINITY, l = 0.f, acc[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = 0.f;
-    for (int q0 = 0; q0 < parts; q0 += 4) {
+    for (int q0 = mine; q0 < parts; q0 += 4 * share) {
       float2 ml[4];
       uint4 o[4];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const int q = min(q0 + s, parts - 1);
+        const int q = min(q0 + s * share, parts - 1);
         const size_t row = at(q) + g;
         ml[s] = (q < n_prefix ? p.prefix_ml : p.own_ml)[row];
         // (a part that saw no key left no row: what is read there is not used)
@@ -816,7 +818,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
       }
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        if (q0 + s >= parts || ml[s].y == 0.f) continue;
+        if (q0 + s * share >= parts || ml[s].y == 0.f) continue;
         const float top = fmaxf(M, ml[s].x);
         const float keep = M == -INFINITY ? 0.f : part_ex2(M - top);
         // (a part whose l is NaN keeps its weight whatever its reference)
@@ -832,6 +834,21 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
           acc[2 * c] = acc[2 * c] * keep + f.x * w;
           acc[2 * c + 1] = acc[2 * c + 1] * keep + f.y * w;
         }
+      }
+    }
+    if (share > 1) {
+#pragma unroll
+      for (int s = kLanes; s < 32; s <<= 1) {
+        const float M2 = __shfl_xor_sync(0xffffffffu, M, s);
+        const float l2 = __shfl_xor_sync(0xffffffffu, l, s), top = fmaxf(M, M2);
+        // (nothing seen, or an l that is NaN: the factor is 1)
+        const float a = M == -INFINITY ? 1.f : part_ex2(M - top);
+        const float b2 = M2 == -INFINITY ? 1.f : part_ex2(M2 - top);
+        M = top;
+        l = l * a + l2 * b2;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          acc[c] = acc[c] * a + __shfl_xor_sync(0xffffffffu, acc[c], s) * b2;
       }
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
