@@ -153,8 +153,9 @@ dflash_status run_prefix(dflash_handle* h, const PrefixPlan& pl, PartParams p, c
   if (s == DFLASH_OK && ctas > 0) s = launch_part<D, 1, 64>(h, tq, tk, tv, own, ctas, st);
   if (s != DFLASH_OK) return s;
   LaunchScope scope(h, DFLASH_KERNEL_PREFIX_COMBINE, st);
-  // a warp a kv group once those fill the card, else a warp a head
-  const int heads = static_cast<int64_t>(p.n_tok) * p.Hkv >= 16 * h->num_sms ? p.G : 1;
+  // a warp a kv group once those fill the card, else a warp a head (1280 tokens of 8
+  // groups: whole calls 396 and 418 us; 512 tokens: 138 and 132)
+  const int heads = static_cast<int64_t>(p.n_tok) * p.Hkv >= 32 * h->num_sms ? p.G : 1;
   const int64_t warps = static_cast<int64_t>(p.n_tok) * (p.Hq / heads);
   launch_k(h->pdl, attn_join_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0,
            st, p, pl.nt, heads, o);
