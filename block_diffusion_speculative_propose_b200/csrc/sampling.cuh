@@ -1372,8 +1372,8 @@ verify_sampled_kernel(const VerifySampledParams p) {
     cluster_sync();
     needed = ld_peer_u32(&sh->more, 0) != 0;
   }
-  smp_arrive();
-  if (!needed) smp_wait();   // rank 0 stays until it has been read
+  if (needed) smp_arrive();
+  else cluster_sync();       // rank 0 stays until every CTA has read its word
   if (needed) {
     const int draft = i < K ? p.drafts[static_cast<int64_t>(b) * K + i] : -1;
     const SmpResult res =
