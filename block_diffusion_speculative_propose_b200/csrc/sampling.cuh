@@ -845,12 +845,15 @@ __device__ __forceinline__ SmpResult smp_draw_row(const SmpRow& r, const SmpBord
             if (w[e] < r.w_min) w[e] = 0;
         }
         if (open) {
-          // what lies before the border's bin is kept; the bin's tokens are listed
+          // what lies before the border's bin is kept; the bin's tokens are listed: the
+          // ones that were counted there, which for weights leaves out those that
+          // weigh nothing (under min_p, and many of them in a flat row)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int side = bd.bins.side(x[e], bd.bin);
             if (side != 0) w[e] = side < 0 ? w[e] : 0;
-            else if (keep(x[e], i + e)) smp_candidate(x[e], r.begin + i + e);
+            else if ((w[e] || !bd.by_mass) && keep(x[e], i + e))
+              smp_candidate(x[e], r.begin + i + e);
             if (side == 0) w[e] = 0;
           }
         } else if (BORDER) {
