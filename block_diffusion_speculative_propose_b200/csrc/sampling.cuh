@@ -341,7 +341,8 @@ __device__ __forceinline__ void smp_add(unsigned* lo, unsigned* hi, u64 w) {
 }
 
 // Which tokens a histogram's weights stand for, at most: bin b's weigh 2^-(t0 + (b +
-// 0.51) dt) of the largest or more.  dt 0: they are counted.
+// 0.51) dt) of the largest or more before they are rounded to integers, so a W is
+// that less a half, and no less than 1.  dt 0: they are counted.
 struct SmpDepth {
   double t0, dt;
 };
@@ -380,9 +381,10 @@ __device__ __noinline__ SmpHit smp_find(int rank, bool by_mass, bool falling, u6
     v += n[1][k] + (static_cast<u64>(n[2][k]) << 32);
   }
   if (!by_mass) v = c;
-  if (!counted && v)
-    c = static_cast<u64>(static_cast<double>(v) *
-                         exp2(depth.t0 + (b + 0.51) * depth.dt - kSmpOneBits)) + 1;
+  if (!counted && v) {
+    const double least = exp2(kSmpOneBits - depth.t0 - (b + 0.51) * depth.dt) - 0.5;
+    c = static_cast<u64>(static_cast<double>(v) / fmax(least, 1.0)) + 1;
+  }
   const u64 run_v = smp_block_scan(v), run_c = smp_block_scan(c);
   if (tid == kSmpThreads - 1)
     for (int k = 0; k < kSmpRanks; ++k) {
@@ -658,7 +660,8 @@ __device__ __forceinline__ SmpBorder smp_at_key(u64 key) {
   return b;
 }
 
-// The border's key, once the bin's tokens are in rank 0's list n_list[1 + which].
+// The border's key, once the bin's tokens are in rank 0's list n_list[1 + which]: the
+// search counted them, or bounded their number, so they all have room.
 __device__ __forceinline__ u64 smp_close(const SmpRow& r, const SmpBorder& bd, int which) {
   SmpShared* sh = smp_shared();
   const int tid = threadIdx.x;
