@@ -8,6 +8,7 @@ library is missing this module raises — there is no fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -252,21 +253,51 @@ def _stream(stream, dev: Optional[int] = None) -> int:
     return int(stream)
 
 
+def _on_stream(stream, device: torch.device):
+    """Context in which a call's stream is the current one: scratch allocated there is
+    that stream's own, and belongs to the graph if the stream is being captured."""
+    if stream is None:
+        if device.index is None or device.index == torch.cuda.current_device():
+            return contextlib.nullcontext()
+        stream = torch.cuda.current_stream(device)
+    return torch.cuda.stream(_stream_object(stream, device))
+
+
+def _stream_object(stream, device: torch.device) -> torch.cuda.Stream:
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+            else torch.cuda.default_stream(device))
+
+
 def _ptr_array(ts: Sequence[torch.Tensor]):
     arr = (ctypes.c_void_p * len(ts))(*[_ptr(t) for t in ts])
     return ctypes.cast(arr, _PP), arr
 
 
 class Workspace:
-    """Device scratch owned by the caller (a uint8 tensor), grown on demand."""
+    """Device scratch owned by the caller (a uint8 tensor), grown on demand.  A buffer
+    belongs to the stream that it was allocated for, so one that is replaced is reused
+    only behind that stream's work; one that another stream, or a capture, has taken
+    too is kept as long as the workspace."""
 
     def __init__(self, device):
         self.device = torch.device(device)
         self.buf = torch.empty(0, dtype=torch.uint8, device=self.device)
+        self._owner, self._shared = None, False
+        self._kept: List[torch.Tensor] = []
 
-    def get(self, nbytes: int) -> torch.Tensor:
-        if self.buf.numel() < nbytes:
-            self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+    def get(self, nbytes: int, stream=None) -> torch.Tensor:
+        """At least ``nbytes`` of scratch for work on ``stream`` (None: the current one)."""
+        with _on_stream(stream, self.device):
+            raw = _stream(None, self.device.index)
+            if self.buf.numel() < nbytes:
+                if self._shared:
+                    self._kept.append(self.buf)
+                self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+                self._owner, self._shared = raw, False
+            if raw != self._owner or torch.cuda.is_current_stream_capturing():
+                self._shared = True
         return self.buf
 
 
@@ -382,7 +413,7 @@ class DFlash:
         _want(positions, torch.int64, "positions")
         _want(slot_mapping, torch.int64, "slot_mapping")
         need = self.inject_workspace_bytes(n) if n else 0
-        ws = workspace if workspace is not None else self.ws.get(need)
+        ws = workspace if workspace is not None else self.ws.get(need, stream)
         kp, ka = _ptr_array(k_cache)
         vp, va = _ptr_array(v_cache)
         _check(lib().dflash_inject_context(self.h, _ptr(aux), _ptr(positions),
@@ -403,7 +434,7 @@ class DFlash:
         if draft_tokens is None:
             draft_tokens = torch.empty(B, bs - 1, dtype=torch.int32, device=self.device)
         need = self.propose_workspace_bytes(B, W) if B else 0
-        ws = workspace if workspace is not None else self.ws.get(need)
+        ws = workspace if workspace is not None else self.ws.get(need, stream)
         kp, ka = _ptr_array(k_cache)
         vp, va = _ptr_array(v_cache)
         _check(lib().dflash_propose(self.h, _ptr(bonus_tokens), _ptr(seq_lens),
@@ -472,7 +503,7 @@ class DFlash:
                                     last_token_indices, num_draft, aux, block_table, k_cache,
                                     v_cache, prev_sampled, prev_num_draft, out, device_error)
         need = self.spec_step_workspace_bytes(io.B, io.n, io.max_pages_per_seq) if io.B else 0
-        ws = workspace if workspace is not None else self.ws.get(need)
+        ws = workspace if workspace is not None else self.ws.get(need, stream)
         _check(lib().dflash_spec_step(self.h, ctypes.byref(io), _ptr(ws), ws.numel(),
                                       _stream(stream)), "dflash_spec_step")
         return o
@@ -509,7 +540,7 @@ class DFlash:
             draft_keys = torch.empty(B, bs - 1, dtype=torch.int64, device=self.device)
         _want(draft_keys, torch.int64, "draft_keys")
         need = self.propose_workspace_bytes(B, W) if B else 0
-        ws = workspace if workspace is not None else self.ws.get(need)
+        ws = workspace if workspace is not None else self.ws.get(need, stream)
         kp, ka = _ptr_array(k_cache)
         vp, va = _ptr_array(v_cache)
         _check(lib().dflash_propose_keys(self.h, _ptr(bonus_tokens), _ptr(seq_lens),
@@ -535,7 +566,7 @@ class DFlash:
         if draft_keys is None:
             draft_keys = torch.empty(B, bs - 1, dtype=torch.int64, device=self.device)
         need = self.propose_workspace_bytes(B, W) if B else 0
-        ws = workspace if workspace is not None else self.ws.get(need)
+        ws = workspace if workspace is not None else self.ws.get(need, stream)
         kp, ka = _ptr_array(k_cache)
         vp, va = _ptr_array(v_cache)
 
@@ -565,7 +596,7 @@ class DFlash:
             bn = block_n or 256
             tiles = -(-M // 128) * -(-N // bn)
             need = max(need, 2 * (tiles * splits + 1) * min(M, 128) * bn * 4)
-        ws = workspace if workspace is not None else self.ws.get(need)
+        ws = workspace if workspace is not None else self.ws.get(need, stream)
         _check(lib().dflash_linear_ex(self.h, _ptr(A), _ptr(W), M, N, K, _ptr(out), block_n,
                                       splits, _ptr(ws), ws.numel(), _stream(stream)),
                "dflash_linear")
@@ -612,7 +643,7 @@ class DFlash:
             o = torch.empty(q.shape[0], q.shape[1] * q.shape[2], dtype=torch.float16,
                             device=self.device)
         need = lib().dflash_attention_workspace_bytes(self.h, B, W) if B else 0
-        ws = workspace if workspace is not None else self.ws.get(need)
+        ws = workspace if workspace is not None else self.ws.get(need, stream)
         _check(lib().dflash_block_attention(self.h, _ptr(q), _ptr(seq_lens), _ptr(block_table),
                                             B, W, _ptr(k_cache), _ptr(v_cache),
                                             int(k_cache.shape[0]), _ptr(o), _ptr(ws),
@@ -649,7 +680,7 @@ class DFlash:
             # a captured call keeps scratch of its graph's own: the handle's may
             # be replaced by a larger one while the graph lives
             ws = (torch.empty(need, dtype=torch.uint8, device=self.device)
-                  if torch.cuda.is_current_stream_capturing() else self.ws.get(need))
+                  if torch.cuda.is_current_stream_capturing() else self.ws.get(need, stream))
         bf, pool = torch.bfloat16, (k_cache.shape[0], hkv, page, d)
         _check(lib().dflash_prefix_attention(
             self.h, _is(q, bf, (n, hq, d), "q", dev), q_len, int(causal),
@@ -770,7 +801,7 @@ class TargetModel:
             logits = torch.empty(n, V, dtype=torch.float32, device=self.device)
         if aux is None and self.n_capture:
             aux = torch.empty(n, self.n_capture * H, dtype=torch.bfloat16, device=self.device)
-        ws = self.ws.get(lib().dflash_target_workspace_bytes(self.h, max(n, 1)))
+        ws = self.ws.get(lib().dflash_target_workspace_bytes(self.h, max(n, 1)), stream)
         _check(lib().dflash_target_forward(self.h, _ptr(tokens), n, int(start_pos), _ptr(logits),
                                            _ptr(aux), _ptr(ws), ws.numel(), _stream(stream)),
                "dflash_target_forward")
