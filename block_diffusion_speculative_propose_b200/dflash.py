@@ -677,10 +677,11 @@ class DFlash:
             if need is None:
                 need = self.prefix_attention_workspace_bytes(*key)
                 self._prefix_bytes[key] = need
-            # a captured call keeps scratch of its graph's own: the handle's may
-            # be replaced by a larger one while the graph lives
-            ws = (torch.empty(need, dtype=torch.uint8, device=self.device)
-                  if torch.cuda.is_current_stream_capturing() else self.ws.get(need, stream))
+            # a captured call has scratch of its graph's own: another graph's may run
+            # while the handle's is in use
+            with _on_stream(stream, self.device):
+                ws = (torch.empty(need, dtype=torch.uint8, device=self.device)
+                      if torch.cuda.is_current_stream_capturing() else self.ws.get(need))
         bf, pool = torch.bfloat16, (k_cache.shape[0], hkv, page, d)
         _check(lib().dflash_prefix_attention(
             self.h, _is(q, bf, (n, hq, d), "q", dev), q_len, int(causal),
@@ -1006,11 +1007,9 @@ def verify_sampled(drafts, target_logits, u_accept, u_sample, temperature=None, 
     if bonus is None:
         bonus = torch.empty(B, dtype=i32, device=device)
     if workspace is None:
-        workspace = torch.empty(max(verify_sampled_workspace_bytes(B, K), 256), dtype=torch.uint8,
-                                device=device)
-        if stream is not None:                # scratch is reused only behind that stream's work
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                    torch.cuda.ExternalStream(int(stream), device=device))
+        with _on_stream(stream, device):      # reused only behind that stream's work
+            workspace = torch.empty(max(verify_sampled_workspace_bytes(B, K), 256),
+                                    dtype=torch.uint8, device=device)
     _check(lib().dflash_verify_sampled(
         _is(drafts, i32, (B, K), "drafts", dev), target_logits.data_ptr(), ld, B, K, V,
         *_settings(B, temperature, top_k, top_p, min_p, dev),

@@ -8,7 +8,7 @@ import contextlib
 import pytest
 import torch
 
-from block_diffusion_speculative_propose_b200 import DFlash, synth
+from block_diffusion_speculative_propose_b200 import DFlash, synth, verify_sampled
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -84,3 +84,53 @@ def test_scratch_that_grows_while_a_stream_is_busy(handle, monkeypatch, kind, ho
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_call_captured_on_a_given_stream_has_its_own_scratch(handle, monkeypatch, raw):
+    small, large = inputs(1, 4), inputs(6, 64)
+    o = call(handle, "prefix", small)
+    want = o.clone()
+    torch.cuda.synchronize()
+    s, other, g = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with Watch(monkeypatch) as w:
+        with torch.cuda.graph(g, stream=s):
+            with torch.cuda.stream(other):         # not the one that is captured
+                call(handle, "prefix", small, o=o, stream=s.cuda_stream if raw else s)
+    held = (handle.ws.buf.data_ptr(), handle.ws.buf.numel())
+    assert len(w.seen) == 1 and w.seen[0][0] != held[0]
+    call(handle, "prefix", large)                  # the handle's own is replaced
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for _, n in (*w.seen, held)
+            for _ in range(8)]
+    o.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
+    assert all(bool((t == 255).all()) for t in junk)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_verification_captured_on_a_given_stream_has_its_own_scratch(raw):
+    B, K, V = 8, 4, 1000
+    logits = torch.randn(B, K + 1, V, device=DEV)
+    drafts = torch.randint(0, V, (B, K), device=DEV, dtype=torch.int32)
+    ua, us = torch.rand(B, K, device=DEV), torch.rand(B, device=DEV)
+    temp = torch.ones(B, device=DEV)
+    outs = verify_sampled(drafts, logits, ua, us, temperature=temp)
+    want = [t.clone() for t in outs]
+    torch.cuda.synchronize()
+    s, other, g = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        with torch.cuda.stream(other):             # not the one that is captured
+            verify_sampled(drafts, logits, ua, us, temperature=temp, out_tokens=outs[0],
+                           num_accepted=outs[1], bonus=outs[2],
+                           stream=s.cuda_stream if raw else s)
+    with torch.cuda.stream(other):                 # whose memory the scratch would be
+        junk = [torch.full((512,), 255, dtype=torch.uint8, device=DEV) for _ in range(64)]
+    torch.cuda.synchronize()
+    for t in outs:
+        t.fill_(-9)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert all(bool((t == 255).all()) for t in junk)
