@@ -242,6 +242,24 @@ def _is(t: torch.Tensor, dtype: torch.dtype, shape, name: str, dev: int) -> int:
     return t.data_ptr()
 
 
+def _bytes(t: torch.Tensor, name: str, dev: int):
+    """(pointer, bytes) of a packed buffer of any type on CUDA device ``dev``."""
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor on the call's CUDA device, "
+                         f"got {t.device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _word(t: Optional[torch.Tensor], name: str, dev: int) -> Optional[int]:
+    """The pointer of a 32-bit word (or more) on CUDA device ``dev``, or None."""
+    if t is None:
+        return None
+    ptr, n = _bytes(t, name, dev)
+    if n < 4 or t.element_size() < 4:
+        raise ValueError(f"{name}: expected a word of 32 bits, got {t.numel()} of {t.dtype}")
+    return ptr
+
+
 def _stream(stream, dev: Optional[int] = None) -> int:
     """A stream's raw handle; None: the current stream, of device ``dev`` if given."""
     if stream is None:
@@ -689,7 +707,7 @@ class DFlash:
             _is(block_table, torch.int32, (B, W), "block_table", dev), B, W, prefix_pages,
             _is(k_cache, bf, pool, "k_cache", dev),
             _is(v_cache, bf, pool, "v_cache", dev), pool[0],
-            _is(o, torch.float16, o.shape, "o", dev), ws.data_ptr(), ws.numel(),
+            _is(o, torch.float16, o.shape, "o", dev), *_bytes(ws, "workspace", dev),
             _stream(stream, dev)),
             "dflash_prefix_attention")
         return o
@@ -975,7 +993,7 @@ def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=Non
         _is(u, torch.float32, (rows,), "u", dev),
         _is(tokens, torch.int32, (rows,), "tokens", dev),
         None if probs is None else _is(probs, torch.float32, (rows,), "probs", dev),
-        _ptr(device_error), _stream(stream, dev)), "dflash_sample_tokens")
+        _word(device_error, "device_error", dev), _stream(stream, dev)), "dflash_sample_tokens")
     return tokens if probs is None else (tokens, probs)
 
 
@@ -1017,8 +1035,8 @@ def verify_sampled(drafts, target_logits, u_accept, u_sample, temperature=None, 
         _is(u_sample, torch.float32, (B,), "u_sample", dev),
         _is(out_tokens, i32, (B, K1), "out_tokens", dev),
         _is(num_accepted, i32, (B,), "num_accepted", dev), _is(bonus, i32, (B,), "bonus", dev),
-        _ptr(device_error), _ptr(workspace), workspace.numel(), _stream(stream, dev)),
-        "dflash_verify_sampled")
+        _word(device_error, "device_error", dev), *_bytes(workspace, "workspace", dev),
+        _stream(stream, dev)), "dflash_verify_sampled")
     return out_tokens, num_accepted, bonus
 
 
