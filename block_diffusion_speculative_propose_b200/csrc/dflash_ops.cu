@@ -74,8 +74,8 @@ PrefixPlan plan_prefix(const dflash_handle* h, int B, int q_len, int W, int pref
     p.tiles = cdiv(prefix_pages * 16, p.kt);
     const int64_t units = static_cast<int64_t>(p.items) * p.tiles;
     // One row tile leaves half of the CTAs that fit to the requests' own keys, and a
-    // CTA at least 256 keys: its start costs as much as six tiles (16 single tokens
-    // over 2048 shared keys, runs of two, four and eight tiles: 23.3, 17.7, 17.7 us).
+    // CTA at least 256 keys: its start costs as much as several tiles (16 single tokens
+    // over 2048 shared keys, runs of two, four and eight tiles: 22.0, 19.3, 21.4 us).
     const int slots = h->num_sms;
     p.too_many = units > INT32_MAX;
     p.run = std::max<int64_t>(p.nt == 2 ? 2 : 4, (units + slots - 1) / slots);
@@ -85,10 +85,10 @@ PrefixPlan plan_prefix(const dflash_handle* h, int B, int q_len, int W, int pref
   const int own_keys = (W - prefix_pages) * 16;
   if (own_keys > 0) {
     // Two CTAs an SM if each has 2048 keys or less, for a CTA's start costs as much
-    // as six tiles (32 requests of up to 2048 own keys in chunks of 448 against 1792:
-    // 147 us against 127); else shorter ones, down to an eighth of an SM's share,
-    // which balance requests of different lengths (100 of up to 8000: chunks of 8192
-    // 398 us, of 5568 325).
+    // as several tiles (32 requests of up to 2048 own keys in chunks of 448 against
+    // 1792: 178 us against 176, with four times the parts); else shorter ones, down to
+    // an eighth of an SM's share, which balance requests of different lengths (100 of
+    // up to 8000: chunks of 8192 417 us, of 5440 378).
     const double per_sm = static_cast<double>(B) * Hkv * own_keys / h->num_sms;
     int chunk = static_cast<int>(std::ceil(std::max(per_sm / 8, std::min(per_sm / 2, 2048.0))));
     chunk = std::max(256, std::min(8192, (chunk + 63) / 64 * 64));
@@ -98,9 +98,9 @@ PrefixPlan plan_prefix(const dflash_handle* h, int B, int q_len, int W, int pref
   }
   const size_t pr = static_cast<size_t>(p.ctas) * p.max_segs * p.nt * 128;
   const size_t ow = static_cast<size_t>(p.splits) * B * Hkv * p.R;
-  p.off_ml = align_up(pr * D * 2);
+  p.off_ml = align_up(pr * D * 4);
   p.off_own = p.off_ml + align_up(pr * 8);
-  p.off_own_ml = p.off_own + align_up(ow * D * 2);
+  p.off_own_ml = p.off_own + align_up(ow * D * 4);
   p.total = p.off_own_ml + align_up(ow * 8) + kAlign;
   return p;
 }
@@ -153,9 +153,10 @@ dflash_status run_prefix(dflash_handle* h, const PrefixPlan& pl, PartParams p, c
   if (s == DFLASH_OK && ctas > 0) s = launch_part<D, 1, 64>(h, tq, tk, tv, own, ctas, st);
   if (s != DFLASH_OK) return s;
   LaunchScope scope(h, DFLASH_KERNEL_PREFIX_COMBINE, st);
-  // a warp a kv group once those fill the card, else a warp a head (1280 tokens of 8
-  // groups: whole calls 396 and 418 us; 512 tokens: 138 and 132)
-  const int heads = static_cast<int64_t>(p.n_tok) * p.Hkv >= 32 * h->num_sms ? p.G : 1;
+  // a warp a kv group once those occupy the card, else a warp a head (tokens of 8
+  // groups, whole calls: 16 21.4 and 18.0 us, 128 91 and 89, 256 63 and 66, 512 168
+  // and 175, 1024 160 and 183)
+  const int heads = static_cast<int64_t>(p.n_tok) * p.Hkv >= 10 * h->num_sms ? p.G : 1;
   const int64_t warps = static_cast<int64_t>(p.n_tok) * (p.Hq / heads);
   launch_k(h->pdl, attn_join_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0,
            st, p, pl.nt, heads, o);
@@ -281,12 +282,12 @@ dflash_status dflash_prefix_attention(dflash_handle* h, const void* q, int q_len
   p.prefix_run = static_cast<unsigned>(pl.run);
   p.row_groups = pl.row_groups;
   p.max_segs = pl.max_segs;
-  p.prefix_o = at<f16>(workspace, 0);
+  p.prefix_o = at<float>(workspace, 0);
   p.prefix_ml = at<float2>(workspace, pl.off_ml);
   p.chunk_keys = pl.chunk;
   p.max_splits = pl.splits;
   p.R = pl.R;
-  p.own_o = at<f16>(workspace, pl.off_own);
+  p.own_o = at<float>(workspace, pl.off_own);
   p.own_ml = at<float2>(workspace, pl.off_own_ml);
   p.scale_log2 =
       static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c.head_dim)));

@@ -4,22 +4,21 @@
 // o = softmax(q K^T / sqrt(D)) V over the keys of a row is a sum over parts of
 // them: with a reference m, l = sum 2^(s - m) and O = sum 2^(s - m) v of each
 // part (s in units of log2), the whole is sum 2^(m - M) O / sum 2^(m - M) l.
-// A part is left as (m, l) in fp32 and O / l in fp16, the output's type: half the
-// bytes of O in fp32, and the rounding (2^-11) is far below that of P (2^-8).  A
-// row with an average past fp16 (the whole may still be inside it) is left in
-// bf16 instead, which -l marks.
-// So the shared prefix is one dense attention of every row of the batch against
-// keys that are read once, each request's own keys are another, and a merge
-// joins them.
-//   prefix   bound by the tensor cores: 4 D flops a row and key, the keys read
+// A part is left as (m, l, O / l) in fp32.  So the shared prefix is one dense
+// attention of every row of the batch against keys that are read once, each
+// request's own keys are another, and a merge joins them.
+//   prefix   bound by the tensor cores: 6 D flops a row and key, the keys read
 //            once per 256 rows from L2
 //   own keys bound by HBM: 4 D bytes a key and kv head
-// P is rounded to bf16 once, 2^-8 of each weight: a second product for what that
-// leaves would add half to the tensor time, five sixths of a large call.
+// P is held as two bf16, the second what the first leaves, and multiplied with V
+// twice (2^-16 of each weight; the 4 D flops of a formula become 6 D).  One bf16,
+// and parts in fp16, leave eight times the error, 1.7e-3 of the result against
+// 2.1e-4, the rounding of the output to fp16 (16, 134 and 447 us for calls of 16, 512
+// and 1280 tokens that now take 18, 176 and 600).
 //
 // attn_part_kernel<D, NT, KT> runs both.  NT row tiles of 128 query rows share
 // the K/V tiles of KT keys that pass through a ring in shared memory; S and,
-// in its place, P (bf16) stay in tensor memory beside O:
+// in its place, P (two bf16) stay in tensor memory beside O:
 //   warp 0      TMA producer: lane j loads page j % (KT / 16), column half j / ..
 //   warp 1      MMA issuer (one thread): S = Q K^T, O += P V with P read from
 //               tensor memory
@@ -29,13 +28,17 @@
 // on one row tile while the other one's softmax runs.  NT = 1: S has two buffers,
 // S(t+1) is issued before P V(t), and a second CTA on the SM fills the rest.
 //
-// Measured at 128 requests x 10 rows over 16384 shared keys (NT = 2): a pair of
-// row tiles takes 3400 cycles a key tile, 2200 of them products (2048 at the full
-// rate); what is left is the chain S, softmax (1640), P V of a row tile.  Tried
-// and slower: an issuer for each row tile (448 us against 347), eight softmax
-// warps a row tile (357), a quarter or half of the exponentials as polynomials on
-// the FMA pipes (347, 373).
-//   NT = 2, KT = 128: one CTA an SM, 4 D x 128 flops per byte read, for many rows
+// Measured at 64 requests x 10 rows over 16384 shared keys (NT = 2): a pair of row
+// tiles takes 5800 cycles a key tile, 3040 of them products; what is left is the chain
+// S, softmax, P V of a row tile, whose softmax shares the exponential units with the
+// other tile's (38 % busy).  With one bf16 a weight 4080 cycles, 2020 products.  Tried
+// with that and slower: an issuer for each row tile (448 us against 347), eight
+// softmax warps a row tile (357), a quarter or half of the exponentials as polynomials
+// on the FMA pipes (347, 373).  With two, calls of 1280 tokens: handing P over in
+// halves (617 us against 605), all high products before the low ones (598 and 596),
+// halves by truncation (605 and 596).
+//   NT = 2, KT = 128: one CTA an SM, 256 flops of the formula per byte read, for
+//                     many rows
 //   NT = 1, KT = 64:  two CTAs an SM, for one request's rows
 #pragma once
 
@@ -59,11 +62,11 @@ struct PartParams {
   int prefix_ctas, prefix_items, prefix_tiles, row_groups;   // row_groups = items per kv head
   unsigned prefix_run;   // units of a CTA; all units fit 31 bits
   int max_segs;
-  f16* prefix_o;       // [prefix_ctas][max_segs][NT][128][D] (bf16 rows where l < 0)
+  float* prefix_o;     // [prefix_ctas][max_segs][NT][128][D]
   float2* prefix_ml;   // [prefix_ctas][max_segs][NT][128]
   // own keys: one CTA a (split, request, kv head)
   int chunk_keys, max_splits, R;          // R = q_len * G
-  f16* own_o;          // [max_splits][B][Hkv][R][D]
+  float* own_o;        // [max_splits][B][Hkv][R][D]
   float2* own_ml;      // [max_splits][B][Hkv][R]
   float scale_log2;
   unsigned* err;
@@ -144,20 +147,15 @@ __device__ __forceinline__ void part_st_x32(uint32_t taddr, const uint32_t* r) {
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void part_st_x16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
-      : "memory");
-}
 // kind::f16, bf16 x bf16 -> fp32; b_mn: B is MN-major.
 __host__ __device__ constexpr uint32_t part_idesc(int M, int N, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
+
+// Column of the weights of keys 16 kk .. 16 kk + 15 of a tile, high halves; the low
+// ones are 16 columns on.
+__device__ __forceinline__ constexpr int part_p_at(int kk) { return (kk >> 1) * 32 + (kk & 1) * 8; }
 
 // Two floats in a 64-bit register: the FMA pipes take both in one instruction.
 typedef unsigned long long f32x2;
@@ -185,12 +183,13 @@ __device__ __forceinline__ float part_max3(float a, float b, float c) {
   return r;
 }
 
-// P = 2^(s scale - ref) in the place of KT of a row's scores, as bf16 pairs; returns
-// their sum.  In chunks of 32 scores: chunk c is read from columns 32 c ..
-// and written to columns 16 c .., never ahead of what is still to be read.
+// P = 2^(s scale - ref) in the place of KT of a row's scores; returns their sum.  Chunk
+// c of 32 scores is read from columns 32 c .. and gives its place to the bf16 pairs
+// of P, and behind them (part_p_at) those of what P leaves.
 template <int KT, bool MASKED>
 __device__ __forceinline__ float part_weights(uint32_t s_at, float scale, float ref, int left) {
   const f32x2 sc2 = part_pack(scale, scale), nr2 = part_pack(-ref, -ref);
+  const f32x2 minus1 = part_pack(-1.f, -1.f);
   f32x2 l2[2] = {part_pack(0.f, 0.f), part_pack(0.f, 0.f)};
   float x[2][32];
   tmem_ld_32x32b_x32(s_at, x[0]);
@@ -198,7 +197,7 @@ __device__ __forceinline__ float part_weights(uint32_t s_at, float scale, float 
 #pragma unroll
   for (int c = 0; c < KT / 32; ++c) {
     if (c + 1 < KT / 32) tmem_ld_32x32b_x32(s_at + (c + 1) * 32, x[(c + 1) & 1]);
-    uint32_t w[16];
+    uint32_t w[32];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       float a = x[c & 1][2 * e], b = x[c & 1][2 * e + 1];
@@ -212,9 +211,14 @@ __device__ __forceinline__ float part_weights(uint32_t s_at, float scale, float 
       b = part_ex2(b);
       l2[e & 1] = part_add2(l2[e & 1], part_pack(a, b));
       w[e] = pack_bf16x2(a, b);
+      part_unpack(part_fma2(part_pack(__uint_as_float(w[e] << 16),
+                                      __uint_as_float(w[e] & 0xffff0000u)),
+                            minus1, part_pack(a, b)),
+                  a, b);
+      w[16 + e] = pack_bf16x2(a, b);
     }
     if (c + 1 < KT / 32) tmem_ld_wait();
-    part_st_x16(s_at + c * 16, w);
+    part_st_x32(s_at + c * 32, w);
   }
   float la, lb;
   part_unpack(part_add2(l2[0], l2[1]), la, lb);
@@ -481,9 +485,11 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
-              part_mma_ts(col_o(i), col_s(buf) + kk * 8, v_at + kk * (16 * 128 / 16), v_hi, id_o,
-                          kk > 0 || t > 0 ? 1u : 0u);
+            for (int kk = 0; kk < KT / 16; ++kk) {
+              const uint32_t p_at = col_s(buf) + part_p_at(kk), v_kk = v_at + kk * (16 * 128 / 16);
+              part_mma_ts(col_o(i), p_at, v_kk, v_hi, id_o, kk > 0 || t > 0 ? 1u : 0u);
+              part_mma_ts(col_o(i), p_at + 16, v_kk, v_hi, id_o, 1u);
+            }
             if (NT == 1) umma_commit(pv_done);
             if (!more) umma_commit(&o_full[i]);
             if (NT == 2 && more) mma_s(i, buf, k_lo + kslot * kSlot);
@@ -534,7 +540,9 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (rows) {
           const uint32_t s_at = col_s(buf) + lanes;
           const int left = limit - (seg.key0 + t * KT);    // keys of the tile that the row sees
-          const bool masked = __any_sync(0xffffffffu, left < KT);
+          // (a CTA of one row tile lives for a few tiles, and its code comes from L2:
+          // one path is quicker than two, 16 single tokens 17.8 us against 19.9)
+          const bool masked = NT == 1 || __any_sync(0xffffffffu, left < KT);
           float mx;
           {
             // S is read twice, for the maximum and for P: the second reading costs
@@ -612,12 +620,11 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       if (ok) ok = mbar_wait(&o_full[i], k & 1, p.err);
       tc_fence_after();
       const bool own = seg.b >= 0;
-      f16* dst = own ? p.own_o + (static_cast<size_t>(seg.slot) * p.R + r) * D
+      float* dst = own ? p.own_o + (static_cast<size_t>(seg.slot) * p.R + r) * D
                        : p.prefix_o + ((static_cast<size_t>(seg.slot) * NT + i) * 128 + r) * D;
       const bool store = ok && rows && l != 0.f &&   // a NaN is a result
                          (!own || r < p.R);
       const float inv = 1.f / l;
-      float big = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         if (!rows) break;
@@ -626,36 +633,12 @@ attn_part_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         tmem_ld_wait();
         if (store) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 w;
-            w.x = pack_f16x2(o[e] * inv, o[e + 1] * inv);
-            w.y = pack_f16x2(o[e + 2] * inv, o[e + 3] * inv);
-            w.z = pack_f16x2(o[e + 4] * inv, o[e + 5] * inv);
-            w.w = pack_f16x2(o[e + 6] * inv, o[e + 7] * inv);
-            *reinterpret_cast<uint4*>(dst + c * 32 + e) = w;
-#pragma unroll
-            for (int a = 0; a < 8; a += 2)
-              big = part_max3(big, fabsf(o[e + a]), fabsf(o[e + a + 1]));
-          }
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(dst + c * 32 + e) =
+                make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
         }
       }
-      // past fp16 (or not finite): the row once more, in bf16
-      const bool wide = store && big * inv > 65504.f;
-      if (__any_sync(0xffffffffu, wide)) {
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
-          tmem_ld_32x32b_x32(col_o(i) + lanes + c * 32, o);
-          tmem_ld_wait();
-          if (wide) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              *reinterpret_cast<uint32_t*>(dst + c * 32 + e) =
-                  pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-          }
-        }
-      }
-      const float2 stats = make_float2(m, wide ? -l : l);
+      const float2 stats = make_float2(m, l);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[i]);
@@ -807,14 +790,17 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     for (int c = 0; c < 8; ++c) acc[c] = 0.f;
     for (int q0 = mine; q0 < parts; q0 += 4 * share) {
       float2 ml[4];
-      uint4 o[4];
+      float4 o[4][2];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const int q = min(q0 + s * share, parts - 1);
         const size_t row = at(q) + g;
         ml[s] = (q < n_prefix ? p.prefix_ml : p.own_ml)[row];
         // (a part that saw no key left no row: what is read there is not used)
-        o[s] = *reinterpret_cast<const uint4*>((q < n_prefix ? p.prefix_o : p.own_o) + row * D + c8);
+        const float4* src = reinterpret_cast<const float4*>(
+            (q < n_prefix ? p.prefix_o : p.own_o) + row * D + c8);
+        o[s][0] = src[0];
+        o[s][1] = src[1];
       }
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
@@ -822,18 +808,12 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         const float top = fmaxf(M, ml[s].x);
         const float keep = M == -INFINITY ? 0.f : part_ex2(M - top);
         // (a part whose l is NaN keeps its weight whatever its reference)
-        const float w =
-            fabsf(ml[s].y) * (ml[s].x == -INFINITY ? 1.f : part_ex2(ml[s].x - top));
+        const float w = ml[s].y * (ml[s].x == -INFINITY ? 1.f : part_ex2(ml[s].x - top));
         M = top;
         l = l * keep + w;
-        const __half2* v = reinterpret_cast<const __half2*>(&o[s]);
-        const __nv_bfloat162* wide = reinterpret_cast<const __nv_bfloat162*>(&o[s]);
+        const float* v = reinterpret_cast<const float*>(o[s]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 f = ml[s].y < 0.f ? __bfloat1622float2(wide[c]) : __half22float2(v[c]);
-          acc[2 * c] = acc[2 * c] * keep + f.x * w;
-          acc[2 * c + 1] = acc[2 * c + 1] * keep + f.y * w;
-        }
+        for (int c = 0; c < 8; ++c) acc[c] = acc[c] * keep + v[c] * w;
       }
     }
     if (share > 1) {
