@@ -28,10 +28,10 @@
 // on one row tile while the other one's softmax runs.  NT = 1: S has two buffers,
 // S(t+1) is issued before P V(t), and a second CTA on the SM fills the rest.
 //
-// Measured at 64 requests x 10 rows over 16384 shared keys (NT = 2): a pair of row
-// tiles takes 5800 cycles a key tile, 3040 of them products; what is left is the chain
+// Measured at 128 requests x 10 rows over 16384 shared keys (NT = 2): a pair of row
+// tiles takes 5500 cycles a key tile, 3100 of them products; what is left is the chain
 // S, softmax, P V of a row tile, whose softmax shares the exponential units with the
-// other tile's (38 % busy).  With one bf16 a weight 4080 cycles, 2020 products.  Tried
+// other tile's (40 % busy).  With one bf16 a weight 4080 cycles, 2020 products.  Tried
 // with that and slower: an issuer for each row tile (448 us against 347), eight
 // softmax warps a row tile (357), a quarter or half of the exponentials as polynomials
 // on the FMA pipes (347, 373).  With two, calls of 1280 tokens: handing P over in

@@ -31,10 +31,11 @@
 // Measured (rows of 151936 unless said otherwise), against reading the rows once:
 //   1 row, top_k 20, top_p 0.8       13 us: the chain of barriers and of 64-bit steps
 //   16 rows of a verify              21 us: the same, and the clearing launch
-//   512 rows of 128256, no filter   141 us: 41; the weights' 64-bit operations
-//   320 rows of 128256, top_p 0.9   147 us: 25; two passes over weights, and the
+//   512 rows of 128256, no filter   142 us: 41; the weights' 64-bit operations
+//   320 rows of 128256, top_p 0.9   142 us: 25; two passes over weights, and the
 //                                   histogram's shared-memory additions
-//   128 rows, mixed filters          79 us: 12; the rows with top_p alone
+//   128 rows, mixed filters          80 us: 12; the rows with top_p alone
+//   128 requests of 16 rows, mixed  200 us: 192; rows behind a refusal are spared
 // A wave is 74 rows (4 CTAs an SM, 8 a row); top_k rows take 20 us of it, rows
 // that need all weights 40 to 75.
 #pragma once
@@ -47,9 +48,9 @@ constexpr int kSmpThreads = 256;
 constexpr int kSmpWarps = kSmpThreads / 32;
 constexpr int kSmpCtas = 4;           // of an SM
 // CTAs of a row (the largest portable cluster).  Four suit a batch of top_k rows
-// better (128 rows 27 us against 37), but a batch whose filters differ waits for
-// its slowest rows (104 against 78), and of a request's rows fewer are spared
-// (128 requests of 16 rows 282 against 207).
+// better (128 rows take 0.73 of the time), but a batch whose filters differ waits
+// for its slowest rows (128 rows 1.33 of it), and of a request's rows fewer are
+// spared (128 requests of 16 rows 1.36 of it).
 constexpr int kSmpRanks = 8;
 constexpr int kSmpBins = kSmpRanks * kSmpThreads;   // of a histogram: each thread merges one
 constexpr int kSmpMaxBins = 1024;     // bins of the threads' maxima
@@ -1360,7 +1361,7 @@ struct VerifySampledParams {
 // request's answer is its first refusing row's, whoever ran.  The cluster that
 // settles a request's last row writes the answer.  (Runs of two, four or eight
 // rows a cluster, which spare launches, took 1.3 to 1.5 times as long at 128
-// requests of 16 rows, 180 us now: the rows of one request then wait in line.)
+// requests of 16 rows: the rows of one request then wait in line.)
 __global__ void __launch_bounds__(kSmpThreads, kSmpCtas)
 verify_sampled_kernel(const VerifySampledParams p) {
   pdl_trigger();
