@@ -11,7 +11,7 @@
 //            once per 256 rows from L2
 //   own keys bound by HBM: 4 D bytes a key and kv head
 // P is held as two bf16, the second what the first leaves, and multiplied with V
-// twice (2^-16 of each weight; the 4 D flops of a formula become 6 D).  One bf16,
+// twice (2^-15 of each weight; the 4 D flops of a formula become 6 D).  One bf16,
 // and parts in fp16, leave eight times the error, 1.7e-3 of the result against
 // 2.1e-4, the rounding of the output to fp16 (16, 134 and 447 us for calls of 16, 512
 // and 1280 tokens that now take 18, 176 and 600).
@@ -35,8 +35,7 @@
 // with that and slower: an issuer for each row tile (448 us against 347), eight
 // softmax warps a row tile (357), a quarter or half of the exponentials as polynomials
 // on the FMA pipes (347, 373).  With two, calls of 1280 tokens: handing P over in
-// halves (617 us against 605), all high products before the low ones (598 and 596),
-// halves by truncation (605 and 596).
+// halves (617 us against 605), all high products before the low ones (598 and 596).
 //   NT = 2, KT = 128: one CTA an SM, 256 flops of the formula per byte read, for
 //                     many rows
 //   NT = 1, KT = 64:  two CTAs an SM, for one request's rows
@@ -177,6 +176,12 @@ __device__ __forceinline__ f32x2 part_add2(f32x2 a, f32x2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// Two floats as bf16, rounded towards zero (lo in the low half).
+__device__ __forceinline__ uint32_t part_cut_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ float part_max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -185,11 +190,14 @@ __device__ __forceinline__ float part_max3(float a, float b, float c) {
 
 // P = 2^(s scale - ref) in the place of KT of a row's scores; returns their sum.  Chunk
 // c of 32 scores is read from columns 32 c .. and gives its place to the bf16 pairs
-// of P, and behind them (part_p_at) those of what P leaves.
+// of P, and behind them (part_p_at) those of what they leave.  The first is cut off, not
+// rounded, and 2^-20 of it is added to the second: both halves of a weight above 0 are
+// above 0, and an infinite V gives what it gives in the formula.
 template <int KT, bool MASKED>
 __device__ __forceinline__ float part_weights(uint32_t s_at, float scale, float ref, int left) {
   const f32x2 sc2 = part_pack(scale, scale), nr2 = part_pack(-ref, -ref);
-  const f32x2 minus1 = part_pack(-1.f, -1.f);
+  constexpr float kBelow = -1.f + 1.f / (1 << 20);
+  const f32x2 minus = part_pack(kBelow, kBelow);
   f32x2 l2[2] = {part_pack(0.f, 0.f), part_pack(0.f, 0.f)};
   float x[2][32];
   tmem_ld_32x32b_x32(s_at, x[0]);
@@ -210,10 +218,10 @@ __device__ __forceinline__ float part_weights(uint32_t s_at, float scale, float 
       a = part_ex2(a);
       b = part_ex2(b);
       l2[e & 1] = part_add2(l2[e & 1], part_pack(a, b));
-      w[e] = pack_bf16x2(a, b);
+      w[e] = part_cut_bf16x2(a, b);
       part_unpack(part_fma2(part_pack(__uint_as_float(w[e] << 16),
                                       __uint_as_float(w[e] & 0xffff0000u)),
-                            minus1, part_pack(a, b)),
+                            minus, part_pack(a, b)),
                   a, b);
       w[16 + e] = pack_bf16x2(a, b);
     }

@@ -668,8 +668,8 @@ dflash_status dflash_block_attention(dflash_handle* h, const void* q, const int3
  * Row i of request b attends to keys [0, seq_lens[b] + q_len), with causal != 0
  * to [0, seq_lens[b] + i + 1); seq_lens[b] may end inside the prefix.  A negative
  * seq_lens[b] marks a padding request: its rows of o stay as they were.
- * Scores and sums in fp32; a weight is held as two bf16 (2^-16 relative to
- * itself), as in dflash_block_attention.  Masked and unused places of the pools may hold
+ * Scores and sums in fp32; a weight is held as two bf16 (2^-15 relative to
+ * itself).  Masked and unused places of the pools may hold
  * anything, NaN too (a row that a masked V which is not finite met is summed
  * again, slowly, over the keys it sees).  Pages outside the pool or past the
  * table (DFLASH_DEVERR_SLOT, DFLASH_DEVERR_TABLE) are not read.

@@ -2,8 +2,8 @@
 dflash_block_attention.
 
 Bound per element, derived: with weights p_k (sum 1) and A = sum p_k |v_k|,
-  - a weight is the sum of two bf16: the first leaves 2^-8 of it, the second 2^-8 of
-    that: 2^-16 A;
+  - a weight is the sum of two bf16: the first is cut off and leaves 2^-7 of it, the
+    second is off by 2^-8 of that, and adds 2^-20: 2^-15 A + 2^-20 A;
   - scores and exponents: 2^-12 A (as in test_gpu_prefix_attention.py);
   - a sum over n <= 4096 keys in fp32 makes 2 n / 16 additions of products, each off by
     2^-23 of what is summed so far: 2^-14 A; joining parts is far below that;
@@ -34,7 +34,7 @@ def test_against_64_bits(hq, hkv, d, q_len, prefix_pages, own, B, causal):
     got = h.prefix_attention(q, seq, table, prefix_pages, kc, vc, causal=causal).double()
     want, mag = reference(q, seq, table, prefix_pages, kc, vc, causal)
     err = (got - want).abs()
-    bound = 2.0 ** -11 * want.abs() + 2.0 ** -25 + (2.0 ** -12 + 2.0 ** -14 + 2.0 ** -16) * mag
+    bound = 2.0 ** -11 * want.abs() + 2.0 ** -25 + (2.0 ** -12 + 2.0 ** -14 + 2.0 ** -15 + 2.0 ** -20) * mag
     assert (err <= bound).all(), float((err / bound).max())
     assert float(err.norm() / want.norm()) <= 3e-4
     assert h.check_device_errors() == 0
@@ -51,3 +51,29 @@ def test_weights_far_above_the_first_keys_lose_nothing():
     got = h.prefix_attention(q, seq, table, 16, kc, vc).double()
     want, _ = reference(q, seq, table, 16, kc, vc, False)
     assert float((got - want).norm() / want.norm()) <= 3e-4
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("hq,hkv,d,q_len", [(32, 8, 128, 1), (32, 8, 128, 16), (4, 2, 64, 3)])
+@pytest.mark.parametrize("key", [5, 70, 200, 255, 256, 300])
+def test_an_infinite_value_that_is_seen(hq, hkv, d, q_len, key, value):
+    """A key's infinite V is infinite in every row that sees it, in that head and column
+    alone (weights are small, equal to 1 and between; none is 0)."""
+    h = handle(hq, hkv, d)
+    q, seq, table, kc, vc = case(hq, hkv, d, q_len, [300, 330, 350], 16, seed=33, spread=0.3)
+    kc[table[0, 0], :, 3] = 0                        # a score of exactly 0
+    for b in range(1 if key < 256 else 3):
+        vc[table[b, key // 16], hkv - 1, key % 16, 7] = value
+    for causal in (False, True):
+        got = h.prefix_attention(q, seq, table, 16, kc, vc, causal=causal).double()
+        want, _ = reference(q, seq, table, 16, kc, vc, causal)
+        inf = want.isinf()
+        assert inf.any() and torch.equal(got[inf], want[inf])
+        err, fin = (got - want)[~inf].abs(), want[~inf]
+        assert float(err.norm() / fin.norm()) <= 3e-4
+    # one key: a weight of exactly 1, whose second half is nothing but the addition
+    q, seq, table, kc, vc = case(hq, hkv, d, 1, [0, 0], 0, seed=34)
+    vc[table[0, 0], 0, 0, 2] = value
+    got = h.prefix_attention(q, seq, table, 0, kc, vc).double()
+    want, _ = reference(q, seq, table, 0, kc, vc, False)
+    assert torch.equal(got.isinf(), want.isinf()) and torch.equal(got[got.isinf()], want[want.isinf()])
