@@ -1150,6 +1150,8 @@ dflash_status create_handle(const dflash_config* cfg, const dflash_weights* w, i
     return s;
   };
   if (cudaSetDevice(device) != cudaSuccess) return fail(DFLASH_ERR_CUDA);
+  // the weights may still be written by queued work, on any stream
+  if (cudaDeviceSynchronize() != cudaSuccess) return fail(DFLASH_ERR_CUDA);
   if (cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return fail(DFLASH_ERR_CUDA);
   int major = 0;
@@ -2285,6 +2287,8 @@ dflash_status dflash_target_create(const dflash_target_config* cfg, const dflash
     return s;
   };
   if (cudaSetDevice(device) != cudaSuccess) return fail(DFLASH_ERR_CUDA);
+  // the weights may still be written by queued work, on any stream
+  if (cudaDeviceSynchronize() != cudaSuccess) return fail(DFLASH_ERR_CUDA);
   const int H = c.hidden, D = c.head_dim, Hq = c.n_q_heads, Hkv = c.n_kv_heads, I = c.intermediate;
   t->embed = w->embed;
   t->final_norm_w = w->final_norm_w;

@@ -150,7 +150,8 @@ typedef struct dflash_handle dflash_handle;
 
 /* Validates the geometry, makes `device` current, packs the weights and builds
  * the RoPE table (cos/sin of pos * theta^(-2i/d), evaluated in double precision
- * on the device).  Synchronizes the device once at the end.  On success *out
+ * on the device).  Synchronizes the device at the start (work queued before, on
+ * any stream, may still write the weights) and at the end.  On success *out
  * receives the handle; on failure *out is NULL and nothing is leaked.
  * Range of the fp16 storage (DFLASH_ERR_RANGE otherwise): every weight copied
  * to fp16 (wq, wk, wv, wo, w_gate, w_up, lm_head) has |w| <= 65504 and at most
